@@ -16,6 +16,11 @@ and the tiled SGEMM's ``xpose_sgemm``, ``xpose_sgemm_ex``,
 addresses as integers.  ``transpose``, ``copy`` and ``sgemm`` are
 conveniences over torch tensors: torch supplies the device memory and the
 stream, nothing else.
+
+The operators of a normalised linear layer in 8-bit floating point
+(``include/linear/xpose_linear.h``: ``fp8_gemm``, ``fp8_quantize``,
+``layer_norm``, ``layer_norm_quantize``, ``layer_norm_backward`` and
+``clip_grad_norm``) are in ``linear.py`` and are names of this package too.
 """
 from __future__ import annotations
 
@@ -474,3 +479,9 @@ def sgemm(a, b, c=None, *, alpha: float = 1.0, beta: float = 0.0,
         # being reused before the call's kernels have run there
         ws.record_stream(stream)
     return c
+
+
+from .linear import (  # noqa: E402  (needs the names above)
+    LINEAR_EXPORTS, LINEAR_POW2, XposeClipTensor, XposeFp8GemmInfo,
+    clip_grad_norm, fp8_gemm, fp8_gemm_plan, fp8_quantize, layer_norm,
+    layer_norm_backward, layer_norm_quantize)

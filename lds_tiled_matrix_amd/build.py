@@ -17,7 +17,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libxpose.so")
 SOURCES = ["xpose_kernels.hip", "xpose_api.cpp", "sgemm_kernels.hip",
-           "sgemm_api.cpp"]
+           "sgemm_api.cpp", "fp8_gemm_kernels.hip", "quantize_kernels.hip",
+           "norm_kernels.hip", "linear_api.cpp"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,152 @@
+// Device helpers shared by the kernels of the FP8 linear layer's operators:
+// vectors of eight elements, sums and maxima over lanes, and the e4m3
+// rounding of x / scale.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace xpose {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Vectors that need no more than their element's alignment: gfx950 loads and
+// stores global memory at any byte address, so rows of odd pitch take the
+// same 16-byte accesses as aligned ones.
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef _Float16 f16x8_any __attribute__((ext_vector_type(8), aligned(2)));
+typedef __bf16 bf16x8_any __attribute__((ext_vector_type(8), aligned(2)));
+
+template <typename T> struct Vec8;
+template <> struct Vec8<float> { f32x4_any v[2]; };
+template <> struct Vec8<_Float16> { f16x8_any v; };
+template <> struct Vec8<__bf16> { bf16x8_any v; };
+
+// Eight elements at p, of which the first `valid` exist; zeros for the rest.
+template <typename T>
+__device__ inline void load8(const T *p, int valid, float (&f)[8]) {
+  if (valid >= 8) {
+    const Vec8<T> r = *reinterpret_cast<const Vec8<T> *>(p);
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = r.v[e / 4][e % 4];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = (float)r.v[e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = e < valid ? (float)p[e] : 0.f;
+  }
+}
+
+template <typename T>
+__device__ inline void store8(T *p, int valid, const float (&f)[8]) {
+  if (valid >= 8) {
+    Vec8<T> r;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r.v[e / 4][e % 4] = f[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r.v[e] = (T)f[e];
+    }
+    *reinterpret_cast<Vec8<T> *>(p) = r;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < valid) p[e] = (T)f[e];
+  }
+}
+
+// ----- over lanes ------------------------------------------------------------
+
+// x of the lane `N` further on in this lane's row of 16 (cyclic).
+template <int N>
+__device__ inline uint32_t rotate16(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x120 + N, 0xf, 0xf,
+                                               true);
+}
+
+// Magnitudes are compared as the integers that their bits are: a NaN is then
+// above infinity, so that it is not lost.
+__device__ inline uint32_t magnitude(float x) {
+  return __float_as_uint(x) & 0x7fffffffu;
+}
+__device__ inline uint32_t max16(uint32_t x) {
+  x = max(x, rotate16<8>(x));
+  x = max(x, rotate16<4>(x));
+  x = max(x, rotate16<2>(x));
+  return max(x, rotate16<1>(x));
+}
+
+// The sum over a wave's 64 lanes, in every lane.
+__device__ inline float sum64(float x) {
+  x += __uint_as_float(rotate16<8>(__float_as_uint(x)));
+  x += __uint_as_float(rotate16<4>(__float_as_uint(x)));
+  x += __uint_as_float(rotate16<2>(__float_as_uint(x)));
+  x += __uint_as_float(rotate16<1>(__float_as_uint(x)));
+  x += __shfl_xor(x, 16);
+  return x + __shfl_xor(x, 32);
+}
+
+// ----- e4m3 --------------------------------------------------------------------
+
+constexpr float kE4m3Max = 448.f;
+constexpr float kSmallestScale = 0x1p-126f;
+
+template <bool POW2>
+__device__ inline float scale_of(uint32_t amax_bits) {
+  float s = __uint_as_float(amax_bits) / kE4m3Max;
+  if (s < kSmallestScale) s = kSmallestScale;  // a NaN stays
+  if (POW2 && s < __builtin_inff())
+    s = __uint_as_float((__float_as_uint(s) + 0x7fffffu) & 0x7f800000u);
+  return s;
+}
+
+// x / scale, rounded to float32 as a division is wherever that decides the
+// e4m3 value, for three multiplications instead of a division's ten.
+//
+// With r = 1 / s correctly rounded, q = x r is off by a little over one unit
+// in the last place; q + (x - q s) r, the remainder exact in a fused
+// multiply-add, is the correctly rounded quotient unless the remainder
+// underflows.  It cannot where it matters: below s = 2^-60 both x and s are
+// taken times 2^64, and with s >= 2^-60 a remainder underflows only where
+// x / s < 2^-40, which is 0 in e4m3 either way.  By a power of two, x r is
+// x / s itself.
+//
+// scale inf: x / inf is 0 for a finite x and NaN for an infinite one, which
+// is x * 0.  scale NaN: everything is NaN.
+template <bool POW2>
+struct Quotient {
+  float up, s, r;
+  __device__ explicit Quotient(float scale) {
+    if (POW2) {
+      r = 1.f / scale;
+    } else {
+      const bool inf = scale == __builtin_inff();
+      up = scale < 0x1p-60f ? 0x1p64f : 1.f;
+      s = inf ? 0.f : scale * up;
+      r = inf ? 0.f : 1.f / s;
+    }
+  }
+  __device__ float operator()(float x) const {
+    if (POW2) return x * r;
+    x *= up;
+    const float q = x * r;
+    // the remainder's negative, so that a zero keeps its sign
+    return __builtin_fmaf(-__builtin_fmaf(q, s, -x), r, q);
+  }
+};
+
+// Four values to e4m3, nearest even; |f| <= 448 or NaN.
+__device__ inline uint32_t e4m3x4(float a, float b, float c, float d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
+
+}  // namespace
+}  // namespace xpose

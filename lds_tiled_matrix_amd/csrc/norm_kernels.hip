@@ -1,0 +1,438 @@
+// gfx950 kernels of layer norm, as a tensor or straight as e4m3 with block
+// scales, and of its backward pass.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/linear/xpose_linear.h"
+#include "linear_device.h"
+#include "linear_kernels.h"
+
+namespace xpose {
+namespace {
+
+// A row stays in the registers of the TR lanes that work on it, NC chunks of
+// eight neighbouring columns a lane: it is read once, and the variance is the
+// mean of the centred squares, not a difference of large sums.
+//
+// TR is 64 (a wave a row, four rows a workgroup) or the whole workgroup.
+
+// Weights and biases: float32, or of the input's 16-bit types.
+__device__ inline void load_param8(const void *p, int dtype, int64_t col, int valid, float none, float (&f)[8]) {
+  if (!p) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = none;
+  } else if (dtype == XPOSE_F32) {
+    load8((const float *)p + col, valid, f);
+  } else if (dtype == XPOSE_F16) {
+    load8((const _Float16 *)p + col, valid, f);
+  } else {
+    load8((const __bf16 *)p + col, valid, f);
+  }
+}
+
+__device__ inline int in_row(int64_t cols, int64_t col) {
+  const int64_t left = cols - col;
+  return left < 0 ? 0 : left > 8 ? 8 : (int)left;
+}
+
+// Sums over the lanes of a row, the same in all of them.  With one wave a row
+// no LDS is needed; else `lds` holds a float for each wave, and two calls in
+// turn use two of them, so that one barrier a call is enough.
+template <int TR>
+__device__ inline float row_sum(float x, float *lds) {
+  x = sum64(x);
+  if constexpr (TR > 64) {
+    if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = x;
+    __syncthreads();
+    x = lds[0];
+#pragma unroll
+    for (int w = 1; w < TR / 64; ++w) x += lds[w];
+  }
+  return x;
+}
+
+enum Out { kTensor, kE4m3, kE4m3Pow2 };
+
+// What a lane does with eight normalised values of one chunk.
+template <typename T, Out OUT>
+__device__ inline void put_chunk(const NormArgs &a, int64_t row, int64_t col, int valid, const float (&y)[8]) {
+  if constexpr (OUT == kTensor) {
+    store8((T *)a.y + row * a.ldy + col, valid, y);
+  } else {
+    // the 16 lanes of a DPP row hold the 128 columns of one block
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, e < valid ? magnitude(y[e]) : 0u);
+    const float scale = scale_of<OUT == kE4m3Pow2>(max16(m));
+    if (threadIdx.x % 16 == 0 && valid > 0) a.scale[(col >> 7) * a.ld_scale + row] = scale;
+    const Quotient<OUT == kE4m3Pow2> by(scale);
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = by(y[e]);
+    const u32x2 w = {e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7])};
+    uint8_t *q = (uint8_t *)a.y + row * a.ldy + col;
+    if (valid == 8) {
+      *reinterpret_cast<u32x2 *>(q) = w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < valid) q[e] = (uint8_t)(w[e / 4] >> (8 * (e % 4)));
+    }
+  }
+}
+
+constexpr int norm_threads(int tr) { return tr == 64 ? 256 : tr; }
+
+template <typename T, Out OUT, int TR, int NC>
+__global__ __launch_bounds__(norm_threads(TR)) void norm_kernel(NormArgs a) {
+  __shared__ float lds[2][TR > 64 ? TR / 64 : 1];
+  const int lane = threadIdx.x % TR;
+  const int64_t row = (int64_t)blockIdx.x * (norm_threads(TR) / TR) + threadIdx.x / TR;
+  if (row >= a.rows) return;  // whole waves, and none where barriers follow
+  const T *x = (const T *)a.x + row * a.ldx;
+  float v[NC][8];
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int64_t col = (i * TR + lane) * 8;
+    load8(x + col, in_row(a.cols, col), v[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += v[i][e];
+  const float mean = row_sum<TR>(s, lds[0]) / (float)a.cols;
+  s = 0.f;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int valid = in_row(a.cols, (i * TR + lane) * 8);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[i][e] = e < valid ? v[i][e] - mean : 0.f;
+      s = __builtin_fmaf(v[i][e], v[i][e], s);
+    }
+  }
+  const float rstd = 1.f / sqrtf(row_sum<TR>(s, lds[1]) / (float)a.cols + a.eps);
+  if (lane == 0 && a.mean) {
+    a.mean[row] = mean;
+    a.rstd[row] = rstd;
+  }
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int64_t col = (i * TR + lane) * 8;
+    const int valid = in_row(a.cols, col);
+    float w[8], b[8], y[8];
+    load_param8(a.weight, a.param_dtype, col, valid, 1.f, w);
+    load_param8(a.bias, a.param_dtype, col, valid, 0.f, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(v[i][e] * rstd, w[e], b[e]);
+    put_chunk<T, OUT>(a, row, col, valid, y);
+  }
+}
+
+// Rows of any length, in three sweeps; the second and third find much of the
+// row in the caches.
+constexpr int kLongThreads = 1024;
+template <typename T, Out OUT>
+__global__ __launch_bounds__(kLongThreads) void norm_long_kernel(NormArgs a) {
+  __shared__ float lds[2][kLongThreads / 64];
+  const int64_t row = blockIdx.x;
+  const T *x = (const T *)a.x + row * a.ldx;
+  constexpr int64_t kStep = kLongThreads * 8;
+  float s = 0.f;
+  for (int64_t col = threadIdx.x * 8; col < a.cols; col += kStep) {
+    float v[8];
+    load8(x + col, in_row(a.cols, col), v);
+    float t = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t += v[e];
+    s += t;
+  }
+  const float mean = row_sum<kLongThreads>(s, lds[0]) / (float)a.cols;
+  s = 0.f;
+  for (int64_t col = threadIdx.x * 8; col < a.cols; col += kStep) {
+    const int valid = in_row(a.cols, col);
+    float v[8];
+    load8(x + col, valid, v);
+    float t = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float d = e < valid ? v[e] - mean : 0.f;
+      t = __builtin_fmaf(d, d, t);
+    }
+    s += t;
+  }
+  const float rstd = 1.f / sqrtf(row_sum<kLongThreads>(s, lds[1]) / (float)a.cols + a.eps);
+  if (threadIdx.x == 0 && a.mean) {
+    a.mean[row] = mean;
+    a.rstd[row] = rstd;
+  }
+  // whole groups of 16 lanes stay together: the block maxima need them all
+  for (int64_t c0 = 0; c0 < a.cols; c0 += kStep) {
+    const int64_t col = c0 + threadIdx.x * 8;
+    const int valid = in_row(a.cols, col);
+    float v[8], w[8], b[8];
+    load8(x + col, valid, v);
+    load_param8(a.weight, a.param_dtype, col, valid, 1.f, w);
+    load_param8(a.bias, a.param_dtype, col, valid, 0.f, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf((v[e] - mean) * rstd, w[e], b[e]);
+    put_chunk<T, OUT>(a, row, col, valid, v);
+  }
+}
+
+hipError_t launch(const void *kernel, const NormArgs &a, uint32_t grid, int threads, hipStream_t s) {
+  NormArgs copy = a;
+  void *args[] = {&copy};
+  return hipLaunchKernel(kernel, dim3(grid), dim3(threads), args, 0, s);
+}
+template <typename T, Out OUT, int TR, int NC>
+hipError_t launch_norm(const NormArgs &a, hipStream_t s) {
+  constexpr int per = norm_threads(TR) / TR;
+  return launch(reinterpret_cast<const void *>(&norm_kernel<T, OUT, TR, NC>), a,
+                (uint32_t)((a.rows + per - 1) / per), norm_threads(TR), s);
+}
+template <typename T, Out OUT>
+hipError_t norm(const NormArgs &a, hipStream_t s) {
+  if (a.cols <= 512) return launch_norm<T, OUT, 64, 1>(a, s);
+  if (a.cols <= 1024) return launch_norm<T, OUT, 64, 2>(a, s);
+  if (a.cols <= 2048) return launch_norm<T, OUT, 256, 1>(a, s);
+  if (a.cols <= 4096) return launch_norm<T, OUT, 256, 2>(a, s);
+  if (a.cols <= 8192) return launch_norm<T, OUT, 512, 2>(a, s);
+  if (a.cols <= 16384) return launch_norm<T, OUT, 1024, 2>(a, s);
+  return launch(reinterpret_cast<const void *>(&norm_long_kernel<T, OUT>), a,
+                (uint32_t)a.rows, kLongThreads, s);
+}
+template <Out OUT>
+hipError_t norm(const NormArgs &a, int dtype, hipStream_t s) {
+  if (dtype == XPOSE_F32) return norm<float, OUT>(a, s);
+  if (dtype == XPOSE_F16) return norm<_Float16, OUT>(a, s);
+  return norm<__bf16, OUT>(a, s);
+}
+
+// ----- the backward pass -----------------------------------------------------
+//
+// A group (a wave or a workgroup, as above) walks over rows `groups` apart and
+// keeps the sums for dweight and dbias of its columns in registers, so dy and
+// x are read once; its two rows of sums go to the workspace, and a second
+// launch adds them up column by column, in a fixed order.
+
+template <typename T, int TR, int NC>
+__global__ __launch_bounds__(norm_threads(TR)) void norm_bwd_kernel(NormBwdArgs a) {
+  __shared__ float lds[2][2][TR > 64 ? TR / 64 : 1];
+  const int lane = threadIdx.x % TR;
+  const int group = blockIdx.x * (norm_threads(TR) / TR) + threadIdx.x / TR;
+  if (group >= a.groups) return;
+  float w[NC][8], dw[NC][8], db[NC][8];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int64_t col = (i * TR + lane) * 8;
+    load_param8(a.weight, a.param_dtype, col, in_row(a.cols, col), 1.f, w[i]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[i][e] = db[i][e] = 0.f;
+  }
+  int turn = 0;
+  for (int64_t row = group; row < a.rows; row += a.groups, turn ^= 1) {
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float dy[NC][8], x[NC][8];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int64_t col = (i * TR + lane) * 8;
+      const int valid = in_row(a.cols, col);
+      load8((const T *)a.dy + row * a.lddy + col, valid, dy[i]);
+      load8((const T *)a.x + row * a.ldx + col, valid, x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[i][e] = (x[i][e] - mean) * rstd;  // times a dy of 0 beyond the row
+        const float g = dy[i][e] * w[i][e];
+        s1 += g;
+        s2 = __builtin_fmaf(g, x[i][e], s2);
+        db[i][e] += dy[i][e];
+        dw[i][e] = __builtin_fmaf(dy[i][e], x[i][e], dw[i][e]);
+      }
+    }
+    // both sums behind one barrier; the next row uses the other half of lds
+    s1 = sum64(s1);
+    s2 = sum64(s2);
+    if constexpr (TR > 64) {
+      if (threadIdx.x % 64 == 0) {
+        lds[turn][0][threadIdx.x / 64] = s1;
+        lds[turn][1][threadIdx.x / 64] = s2;
+      }
+      __syncthreads();
+      s1 = lds[turn][0][0];
+      s2 = lds[turn][1][0];
+#pragma unroll
+      for (int v = 1; v < TR / 64; ++v) {
+        s1 += lds[turn][0][v];
+        s2 += lds[turn][1][v];
+      }
+    }
+    s1 /= (float)a.cols;
+    s2 /= (float)a.cols;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int64_t col = (i * TR + lane) * 8;
+      float d[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        d[e] = (dy[i][e] * w[i][e] - s1 - x[i][e] * s2) * rstd;
+      store8((T *)a.dx + row * a.lddx + col, in_row(a.cols, col), d);
+    }
+  }
+  float *p = a.partial + (int64_t)group * 2 * a.cols;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int64_t col = (i * TR + lane) * 8;
+    const int valid = in_row(a.cols, col);
+    store8(p + col, valid, dw[i]);
+    store8(p + a.cols + col, valid, db[i]);
+  }
+}
+
+// Rows of any length: their two sums first, then blocks of columns.
+template <typename T>
+__global__ __launch_bounds__(kLongThreads) void norm_bwd_sums_kernel(NormBwdArgs a) {
+  __shared__ float lds[2][kLongThreads / 64];
+  const int64_t row = blockIdx.x;
+  const float mean = a.mean[row], rstd = a.rstd[row];
+  float s1 = 0.f, s2 = 0.f;
+  for (int64_t col = threadIdx.x * 8; col < a.cols; col += kLongThreads * 8) {
+    const int valid = in_row(a.cols, col);
+    float dy[8], x[8], w[8], t1 = 0.f, t2 = 0.f;
+    load8((const T *)a.dy + row * a.lddy + col, valid, dy);
+    load8((const T *)a.x + row * a.ldx + col, valid, x);
+    load_param8(a.weight, a.param_dtype, col, valid, 1.f, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float g = dy[e] * w[e];
+      t1 += g;
+      t2 = __builtin_fmaf(g, (x[e] - mean) * rstd, t2);
+    }
+    s1 += t1;
+    s2 += t2;
+  }
+  s1 = row_sum<kLongThreads>(s1, lds[0]);
+  s2 = row_sum<kLongThreads>(s2, lds[1]);
+  if (threadIdx.x == 0) {
+    a.partial[2 * row] = s1 / (float)a.cols;
+    a.partial[2 * row + 1] = s2 / (float)a.cols;
+  }
+}
+
+constexpr int kLongBlock = 2048;  // columns of a workgroup of 256
+template <typename T>
+__global__ __launch_bounds__(256) void norm_bwd_long_kernel(NormBwdArgs a) {
+  const int64_t blocks = (a.cols + kLongBlock - 1) / kLongBlock;
+  const int64_t col = (int64_t)(blockIdx.x % blocks) * kLongBlock + threadIdx.x * 8;
+  const int group = (int)(blockIdx.x / blocks);
+  const int valid = in_row(a.cols, col);
+  float w[8], dw[8] = {}, db[8] = {};
+  load_param8(a.weight, a.param_dtype, col, valid, 1.f, w);
+  for (int64_t row = group; row < a.rows; row += a.groups) {
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    const float s1 = a.partial[2 * row], s2 = a.partial[2 * row + 1];
+    float dy[8], x[8], d[8];
+    load8((const T *)a.dy + row * a.lddy + col, valid, dy);
+    load8((const T *)a.x + row * a.ldx + col, valid, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float xhat = (x[e] - mean) * rstd;
+      d[e] = (dy[e] * w[e] - s1 - xhat * s2) * rstd;
+      db[e] += dy[e];
+      dw[e] = __builtin_fmaf(dy[e], xhat, dw[e]);
+    }
+    store8((T *)a.dx + row * a.lddx + col, valid, d);
+  }
+  float *p = a.partial + 2 * a.rows + (int64_t)group * 2 * a.cols;
+  store8(p + col, valid, dw);
+  store8(p + a.cols + col, valid, db);
+}
+
+// 64 columns a workgroup: lane l of a wave has column l, the four waves every
+// fourth partial sum; both gradients in turn.
+__global__ __launch_bounds__(256) void norm_bwd_params_kernel(NormBwdArgs a) {
+  __shared__ float lds[4][64];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int64_t blocks = (a.cols + 63) / 64;
+  const int which = blockIdx.x >= blocks;
+  const int64_t col = (int64_t)(blockIdx.x - which * blocks) * 64 + lane;
+  float *out = which ? a.dbias : a.dweight;
+  if (!out) return;
+  float s = 0.f;
+  if (col < a.cols) {
+    const float *p = a.partial + which * a.cols + col;
+#pragma unroll 8
+    for (int g = wave; g < a.groups; g += 4) s += p[(int64_t)g * 2 * a.cols];
+  }
+  lds[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && col < a.cols)
+    out[col] = (lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane]);
+}
+
+constexpr int64_t kLongBwd = 8192;  // more would spill registers
+
+hipError_t launch(const void *kernel, const NormBwdArgs &a, int64_t grid, int threads, hipStream_t s) {
+  NormBwdArgs copy = a;
+  void *args[] = {&copy};
+  return hipLaunchKernel(kernel, dim3((uint32_t)grid), dim3(threads), args, 0, s);
+}
+template <typename T, int TR, int NC>
+hipError_t launch_bwd(const NormBwdArgs &a, hipStream_t s) {
+  constexpr int per = norm_threads(TR) / TR;
+  return launch(reinterpret_cast<const void *>(&norm_bwd_kernel<T, TR, NC>), a,
+                (a.groups + per - 1) / per, norm_threads(TR), s);
+}
+template <typename T>
+hipError_t norm_bwd(const NormBwdArgs &a, hipStream_t s) {
+  if (a.cols <= 512) return launch_bwd<T, 64, 1>(a, s);
+  if (a.cols <= 1024) return launch_bwd<T, 64, 2>(a, s);
+  if (a.cols <= 2048) return launch_bwd<T, 256, 1>(a, s);
+  if (a.cols <= 4096) return launch_bwd<T, 256, 2>(a, s);
+  if (a.cols <= kLongBwd) return launch_bwd<T, 512, 2>(a, s);
+  hipError_t e = launch(reinterpret_cast<const void *>(&norm_bwd_sums_kernel<T>), a, a.rows, kLongThreads, s);
+  if (e != hipSuccess) return e;
+  return launch(reinterpret_cast<const void *>(&norm_bwd_long_kernel<T>), a,
+                (a.cols + kLongBlock - 1) / kLongBlock * a.groups, 256, s);
+}
+
+}  // namespace
+
+hipError_t launch_layer_norm(const NormArgs &a, int dtype, hipStream_t s) {
+  return norm<kTensor>(a, dtype, s);
+}
+hipError_t launch_layer_norm_quantize(const NormArgs &a, int dtype, bool pow2, hipStream_t s) {
+  return pow2 ? norm<kE4m3Pow2>(a, dtype, s) : norm<kE4m3>(a, dtype, s);
+}
+
+// Enough groups that every compute unit has loads under way, few enough that
+// their sums are little next to dy and x.
+int norm_bwd_groups(int64_t rows, int64_t cols) {
+  const int64_t most = cols <= 1024 ? 4096 : cols <= 4096 ? 1024 : 512;
+  return (int)(rows < most ? rows : most);
+}
+int64_t norm_bwd_row_floats(int64_t rows, int64_t cols) {
+  return cols > kLongBwd ? 2 * rows : 0;
+}
+
+hipError_t launch_layer_norm_backward(const NormBwdArgs &a, int dtype, hipStream_t s) {
+  if (a.rows > 0) {
+    const hipError_t e = dtype == XPOSE_F32   ? norm_bwd<float>(a, s)
+                         : dtype == XPOSE_F16 ? norm_bwd<_Float16>(a, s)
+                                              : norm_bwd<__bf16>(a, s);
+    if (e != hipSuccess) return e;
+  }
+  if (!a.dweight && !a.dbias) return hipSuccess;
+  NormBwdArgs sums = a;
+  if (a.rows > 0) sums.partial += norm_bwd_row_floats(a.rows, a.cols);
+  return launch(reinterpret_cast<const void *>(&norm_bwd_params_kernel), sums,
+                2 * ((a.cols + 63) / 64), 256, s);
+}
+
+}  // namespace xpose

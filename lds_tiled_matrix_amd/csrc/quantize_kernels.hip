@@ -1,0 +1,314 @@
+// gfx950 kernels of block quantisation to e4m3 and of the clipping of many
+// gradients by their global norm.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/linear/xpose_linear.h"
+#include "linear_device.h"
+#include "linear_kernels.h"
+
+namespace xpose {
+namespace {
+
+// ----- quantisation ------------------------------------------------------------
+//
+// One workgroup takes a tile of 128 x 128, which holds whole blocks of the
+// matrix and of its transpose: x is read once for both.  A lane holds 8 x 8
+// values (rows 8 g .. 8 g + 7, columns 8 c .. 8 c + 7; 16 lanes cover a row,
+// a wave 32 rows), so a row's block is a maximum over 16 lanes, a column's
+// one over the 16 row groups (four in a wave, four waves through LDS), and
+// either direction's bytes are eight of the lane's own.  Rows are stored from
+// registers, 128 bytes a row; the transpose goes through LDS as bytes
+// (16 KiB), in units of 8 rows whose place in a row of the transpose is
+// swizzled by c: writes of 16 lanes (one g, all c) and 16-byte reads then
+// both touch every bank once.
+constexpr int kTile = 128;
+constexpr int kQuantThreads = 256;
+
+template <typename T, int BLOCK_ROWS, bool POW2, bool BOTH>
+__global__ __launch_bounds__(kQuantThreads) void quantize_kernel(QuantizeArgs a) {
+  __shared__ uint32_t col_max[4][kTile];
+  __shared__ __align__(16) uint8_t turned[BOTH ? kTile * kTile : 16];
+  const int t = threadIdx.x, c = t % 16, g = t / 16, wave = t / 64;
+  const int64_t r0 = (int64_t)(blockIdx.x / a.tiles_c) * kTile;
+  const int64_t c0 = (int64_t)(blockIdx.x % a.tiles_c) * kTile;
+  const int64_t row = r0 + 8 * g, col = c0 + 8 * c;
+  const int rows = (int)(a.rows - row < 0 ? 0 : a.rows - row > 8 ? 8 : a.rows - row);
+  const int cols = (int)(a.cols - col < 0 ? 0 : a.cols - col > 8 ? 8 : a.cols - col);
+
+  float x[8][8];
+  const T *src = (const T *)a.x + row * a.ldx + col;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    load8(src + i * a.ldx, i < rows ? cols : 0, x[i]);
+
+  uint32_t row_amax[8], tile_amax = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, magnitude(x[i][j]));
+    row_amax[i] = m;
+    tile_amax = max(tile_amax, m);
+  }
+
+  uint8_t *q = a.q + row * a.ldq + col;
+  const int64_t rb = blockIdx.x / a.tiles_c, cb = blockIdx.x % a.tiles_c;
+  // The bytes of one row (or column) of the lane's values.
+  auto put_row = [&](int i, const float (&f)[8]) {
+    if (i >= rows || cols <= 0) return;
+    const u32x2 w = {e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7])};
+    uint8_t *p = q + i * a.ldq;
+    if (cols == 8) {
+      *reinterpret_cast<u32x2 *>(p) = w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < cols) p[j] = (uint8_t)(w[j / 4] >> (8 * (j % 4)));
+    }
+  };
+  auto put_turned = [&](int j, const float (&f)[8]) {
+    const u32x2 w = {e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7])};
+    const int unit = ((((g >> 1) ^ c) & 7) << 1) | ((g ^ (c >> 3)) & 1);
+    *reinterpret_cast<u32x2 *>(turned + (8 * c + j) * kTile + unit * 8) = w;
+  };
+
+  if constexpr (BLOCK_ROWS == 128) {
+    uint32_t m = max16(tile_amax);
+    m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+    if (t % 64 == 0) col_max[wave][0] = m;
+    __syncthreads();
+    m = max(max(col_max[0][0], col_max[1][0]), max(col_max[2][0], col_max[3][0]));
+    const float scale = scale_of<POW2>(m);
+    if (t == 0) {
+      a.scale[cb * a.ld_scale + rb] = scale;
+      if (BOTH) a.scale_t[rb * a.ld_scale_t + cb] = scale;
+    }
+    const Quotient<POW2> by(scale);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[i][j] = by(x[i][j]);
+      put_row(i, x[i]);
+    }
+    if constexpr (BOTH) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float f[8] = {x[0][j], x[1][j], x[2][j], x[3][j],
+                            x[4][j], x[5][j], x[6][j], x[7][j]};
+        put_turned(j, f);
+      }
+    }
+  } else {
+    if constexpr (BOTH) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, magnitude(x[i][j]));
+        m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+        m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+        if (t % 64 < 16) col_max[wave][8 * c + j] = m;
+      }
+    }
+    float row_scale = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float scale = scale_of<POW2>(max16(row_amax[i]));
+      if (c == i) row_scale = scale;
+      const Quotient<POW2> by(scale);
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = by(x[i][j]);
+      put_row(i, f);
+    }
+    // lanes c < 8 of a row group hold its eight scales
+    if (c < rows) a.scale[cb * a.ld_scale + row + c] = row_scale;
+    if constexpr (BOTH) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int at = 8 * c + j;
+        const float scale = scale_of<POW2>(max(max(col_max[0][at], col_max[1][at]),
+                                               max(col_max[2][at], col_max[3][at])));
+        if (g == j && j < cols) a.scale_t[rb * a.ld_scale_t + col + j] = scale;
+        const Quotient<POW2> by(scale);
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = by(x[i][j]);
+        put_turned(j, f);
+      }
+    }
+  }
+
+  if constexpr (BOTH) {
+    __syncthreads();
+    // 8 lanes a row of the transpose, 16 bytes (two units) each
+    const int p = t % 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = 32 * i + t / 8;
+      const int unit = p ^ ((at >> 3) & 7);
+      u32x4 w = *reinterpret_cast<const u32x4 *>(turned + at * kTile + unit * 16);
+      if (at >= 64) w = {w[2], w[3], w[0], w[1]};
+      const int64_t qrow = c0 + at, qcol = r0 + 16 * p;
+      if (qrow >= a.cols || qcol >= a.rows) continue;
+      uint8_t *dst = a.qt + qrow * a.ldqt + qcol;
+      if (qcol + 16 <= a.rows) {
+        // rows of the transpose start at multiples of 8
+        *reinterpret_cast<u32x2 *>(dst) = u32x2{w[0], w[1]};
+        *reinterpret_cast<u32x2 *>(dst + 8) = u32x2{w[2], w[3]};
+      } else {
+        const int n = (int)(a.rows - qcol);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (e < n) dst[e] = (uint8_t)(w[e / 4] >> (8 * (e % 4)));
+      }
+    }
+  }
+}
+
+template <typename T, int BLOCK_ROWS, bool POW2, bool BOTH>
+hipError_t quantize(const QuantizeArgs &a, hipStream_t s) {
+  QuantizeArgs copy = a;
+  void *args[] = {&copy};
+  return hipLaunchKernel(
+      reinterpret_cast<const void *>(&quantize_kernel<T, BLOCK_ROWS, POW2, BOTH>),
+      dim3(a.tiles_r * a.tiles_c), dim3(kQuantThreads), args, 0, s);
+}
+template <typename T, int BLOCK_ROWS>
+hipError_t quantize(const QuantizeArgs &a, bool pow2, hipStream_t s) {
+  if (pow2)
+    return a.qt ? quantize<T, BLOCK_ROWS, true, true>(a, s)
+                : quantize<T, BLOCK_ROWS, true, false>(a, s);
+  return a.qt ? quantize<T, BLOCK_ROWS, false, true>(a, s)
+              : quantize<T, BLOCK_ROWS, false, false>(a, s);
+}
+template <typename T>
+hipError_t quantize(const QuantizeArgs &a, int block_rows, bool pow2, hipStream_t s) {
+  return block_rows == 1 ? quantize<T, 1>(a, pow2, s) : quantize<T, 128>(a, pow2, s);
+}
+
+// ----- clipping ------------------------------------------------------------------
+//
+// Two launches: every workgroup sums the squares of its chunks into one
+// number, then every workgroup adds up all of those in the same order (16 KiB
+// from the L2 cache) and scales its chunks.  Squares and sums are of 64 bits:
+// no square overflows, and the sum of 10^9 gradients loses nothing; their
+// cost hides behind the loads.  The second launch walks backwards, so that it
+// begins with what the first one left in the caches.
+constexpr int kClipThreads = 256;
+
+struct Span {
+  int tensor;
+  int64_t begin, count;
+};
+
+__device__ inline Span chunk_span(const ClipArgs &a, uint32_t chunk) {
+  int lo = 0, hi = a.tensors - 1;  // the first tensor whose chunks end after it
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (a.end[mid] > chunk) hi = mid; else lo = mid + 1;
+  }
+  const uint32_t first = lo ? a.end[lo - 1] : 0;
+  const int64_t begin = (int64_t)(chunk - first) * kClipChunk;
+  const int64_t rest = a.count[lo] - begin;
+  return {lo, begin, rest < kClipChunk ? rest : kClipChunk};
+}
+
+__device__ inline double sum256(double x, double *lds) {
+#pragma unroll
+  for (int d = 32; d; d /= 2) x += __shfl_xor(x, d);
+  __syncthreads();
+  if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = x;
+  __syncthreads();
+  return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
+template <typename T>
+__device__ inline double squares(const T *p, int64_t count) {
+  double s = 0;
+  for (int64_t i = threadIdx.x * 8; i < count; i += kClipThreads * 8) {
+    float f[8];
+    load8(p + i, count - i < 8 ? (int)(count - i) : 8, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = __builtin_fma((double)f[e], (double)f[e], s);
+  }
+  return s;
+}
+
+__global__ __launch_bounds__(kClipThreads) void clip_squares_kernel(ClipArgs a) {
+  __shared__ double lds[4];
+  double s = 0;
+  for (uint32_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
+    const Span p = chunk_span(a, chunk);
+    const void *in = a.in[p.tensor];
+    if (a.dtype[p.tensor] == XPOSE_F32)
+      s += squares((const float *)in + p.begin, p.count);
+    else if (a.dtype[p.tensor] == XPOSE_F16)
+      s += squares((const _Float16 *)in + p.begin, p.count);
+    else
+      s += squares((const __bf16 *)in + p.begin, p.count);
+  }
+  s = sum256(s, lds);
+  if (threadIdx.x == 0) a.partial[a.first + blockIdx.x] = s;
+}
+
+template <typename T>
+__device__ inline void scale_span(const T *in, T *out, int64_t count, float factor) {
+  for (int64_t i = threadIdx.x * 8; i < count; i += kClipThreads * 8) {
+    const int valid = count - i < 8 ? (int)(count - i) : 8;
+    float f[8];
+    load8(in + i, valid, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= factor;
+    store8(out + i, valid, f);
+  }
+}
+
+__global__ __launch_bounds__(kClipThreads) void clip_scale_kernel(ClipArgs a) {
+  __shared__ double lds[4];
+  double s = 0;
+  for (int i = threadIdx.x; i < a.partials; i += kClipThreads) s += a.partial[i];
+  const double norm = sqrt(sum256(s, lds));
+  double factor = a.max_norm / (norm + a.eps);
+  if (factor > 1.0) factor = 1.0;  // a NaN stays
+  if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
+  for (uint32_t i = blockIdx.x; i < a.chunks; i += gridDim.x) {
+    const Span p = chunk_span(a, a.chunks - 1 - i);
+    const void *in = a.in[p.tensor];
+    void *out = a.out[p.tensor];
+    if (a.dtype[p.tensor] == XPOSE_F32)
+      scale_span((const float *)in + p.begin, (float *)out + p.begin, p.count, (float)factor);
+    else if (a.dtype[p.tensor] == XPOSE_F16)
+      scale_span((const _Float16 *)in + p.begin, (_Float16 *)out + p.begin, p.count, (float)factor);
+    else
+      scale_span((const __bf16 *)in + p.begin, (__bf16 *)out + p.begin, p.count, (float)factor);
+  }
+}
+
+hipError_t launch_clip(const void *kernel, const ClipArgs &a, uint32_t groups, hipStream_t s) {
+  ClipArgs copy = a;
+  void *args[] = {&copy};
+  return hipLaunchKernel(kernel, dim3(groups), dim3(kClipThreads), args, 0, s);
+}
+
+}  // namespace
+
+hipError_t launch_quantize(const QuantizeArgs &a, int dtype, int block_rows,
+                           bool pow2, hipStream_t s) {
+  if (dtype == XPOSE_F32) return quantize<float>(a, block_rows, pow2, s);
+  if (dtype == XPOSE_F16) return quantize<_Float16>(a, block_rows, pow2, s);
+  return quantize<__bf16>(a, block_rows, pow2, s);
+}
+
+hipError_t launch_clip_squares(const ClipArgs &a, uint32_t groups, hipStream_t s) {
+  return launch_clip(reinterpret_cast<const void *>(&clip_squares_kernel), a, groups, s);
+}
+hipError_t launch_clip_scale(const ClipArgs &a, uint32_t groups, hipStream_t s) {
+  return launch_clip(reinterpret_cast<const void *>(&clip_scale_kernel), a, groups, s);
+}
+
+}  // namespace xpose
