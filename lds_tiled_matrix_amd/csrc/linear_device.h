@@ -26,21 +26,27 @@ template <> struct Vec8<_Float16> { f16x8_any v; };
 template <> struct Vec8<__bf16> { bf16x8_any v; };
 
 // Eight elements at p, of which the first `valid` exist; zeros for the rest.
+// As they are in memory: 16-bit types take half of float32's registers.
+template <typename T>
+__device__ inline Vec8<T> load_raw8(const T *p, int valid) {
+  if (valid >= 8) return *reinterpret_cast<const Vec8<T> *>(p);
+  Vec8<T> r;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const T v = e < valid ? p[e] : (T)0.f;
+    if constexpr (sizeof(T) == 4) r.v[e / 4][e % 4] = v; else r.v[e] = v;
+  }
+  return r;
+}
+template <typename T>
+__device__ inline float at8(const Vec8<T> &r, int e) {
+  if constexpr (sizeof(T) == 4) return r.v[e / 4][e % 4]; else return (float)r.v[e];
+}
 template <typename T>
 __device__ inline void load8(const T *p, int valid, float (&f)[8]) {
-  if (valid >= 8) {
-    const Vec8<T> r = *reinterpret_cast<const Vec8<T> *>(p);
-    if constexpr (sizeof(T) == 4) {
+  const Vec8<T> r = load_raw8(p, valid);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = r.v[e / 4][e % 4];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = (float)r.v[e];
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = e < valid ? (float)p[e] : 0.f;
-  }
+  for (int e = 0; e < 8; ++e) f[e] = at8<T>(r, e);
 }
 
 template <typename T>
@@ -123,19 +129,22 @@ __device__ inline float scale_of(uint32_t amax_bits) {
 template <bool POW2>
 struct Quotient {
   float up, s, r;
-  __device__ explicit Quotient(float scale) {
+  bool tiny;  // whether any lane of the wave has up != 1 for its sake
+  __device__ Quotient(float scale, uint32_t amax_bits) {
     if (POW2) {
       r = 1.f / scale;
     } else {
       const bool inf = scale == __builtin_inff();
       up = scale < 0x1p-60f ? 0x1p64f : 1.f;
+      tiny = __any(scale < 0x1p-60f && amax_bits != 0);  // zeros need no care
+      if (!tiny) up = 1.f;
       s = inf ? 0.f : scale * up;
       r = inf ? 0.f : 1.f / s;
     }
   }
   __device__ float operator()(float x) const {
     if (POW2) return x * r;
-    x *= up;
+    if (tiny) x *= up;
     const float q = x * r;
     // the remainder's negative, so that a zero keeps its sign
     return __builtin_fmaf(-__builtin_fmaf(q, s, -x), r, q);

@@ -64,9 +64,10 @@ __device__ inline void put_chunk(const NormArgs &a, int64_t row, int64_t col, in
     uint32_t m = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) m = max(m, e < valid ? magnitude(y[e]) : 0u);
-    const float scale = scale_of<OUT == kE4m3Pow2>(max16(m));
+    m = max16(m);
+    const float scale = scale_of<OUT == kE4m3Pow2>(m);
     if (threadIdx.x % 16 == 0 && valid > 0) a.scale[(col >> 7) * a.ld_scale + row] = scale;
-    const Quotient<OUT == kE4m3Pow2> by(scale);
+    const Quotient<OUT == kE4m3Pow2> by(scale, m);
     float f[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = by(y[e]);
@@ -232,18 +233,34 @@ __global__ __launch_bounds__(norm_threads(TR)) void norm_bwd_kernel(NormBwdArgs 
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[i][e] = db[i][e] = 0.f;
   }
-  int turn = 0;
-  for (int64_t row = group; row < a.rows; row += a.groups, turn ^= 1) {
-    const float mean = a.mean[row], rstd = a.rstd[row];
-    float dy[NC][8], x[NC][8];
-    float s1 = 0.f, s2 = 0.f;
+  // the next row's loads are under way while this one is worked on
+  Vec8<T> next_dy[NC], next_x[NC];
+  float next_mean, next_rstd;
+  auto fetch = [&](int64_t row) {
+    next_mean = a.mean[row];
+    next_rstd = a.rstd[row];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int64_t col = (i * TR + lane) * 8;
       const int valid = in_row(a.cols, col);
-      load8((const T *)a.dy + row * a.lddy + col, valid, dy[i]);
-      load8((const T *)a.x + row * a.ldx + col, valid, x[i]);
+      next_dy[i] = load_raw8((const T *)a.dy + row * a.lddy + col, valid);
+      next_x[i] = load_raw8((const T *)a.x + row * a.ldx + col, valid);
     }
+  };
+  fetch(group);
+  int turn = 0;
+  for (int64_t row = group; row < a.rows; row += a.groups, turn ^= 1) {
+    const float mean = next_mean, rstd = next_rstd;
+    float dy[NC][8], x[NC][8];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        dy[i][e] = at8<T>(next_dy[i], e);
+        x[i][e] = at8<T>(next_x[i], e);
+      }
+    if (row + a.groups < a.rows) fetch(row + a.groups);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
 #pragma unroll
@@ -354,10 +371,11 @@ __global__ __launch_bounds__(256) void norm_bwd_long_kernel(NormBwdArgs a) {
   store8(p + a.cols + col, valid, db);
 }
 
-// 64 columns a workgroup: lane l of a wave has column l, the four waves every
-// fourth partial sum; both gradients in turn.
-__global__ __launch_bounds__(256) void norm_bwd_params_kernel(NormBwdArgs a) {
-  __shared__ float lds[4][64];
+// 64 columns of one gradient a workgroup: lane l of a wave has column l, the
+// 16 waves every 16th partial sum.
+constexpr int kParamWaves = 16;
+__global__ __launch_bounds__(64 * kParamWaves) void norm_bwd_params_kernel(NormBwdArgs a) {
+  __shared__ float lds[kParamWaves][64];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const int64_t blocks = (a.cols + 63) / 64;
   const int which = blockIdx.x >= blocks;
@@ -368,12 +386,15 @@ __global__ __launch_bounds__(256) void norm_bwd_params_kernel(NormBwdArgs a) {
   if (col < a.cols) {
     const float *p = a.partial + which * a.cols + col;
 #pragma unroll 8
-    for (int g = wave; g < a.groups; g += 4) s += p[(int64_t)g * 2 * a.cols];
+    for (int g = wave; g < a.groups; g += kParamWaves) s += p[(int64_t)g * 2 * a.cols];
   }
   lds[wave][lane] = s;
   __syncthreads();
-  if (wave == 0 && col < a.cols)
-    out[col] = (lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane]);
+  if (wave == 0 && col < a.cols) {
+#pragma unroll
+    for (int v = 1; v < kParamWaves; ++v) s += lds[v][lane];
+    out[col] = s;
+  }
 }
 
 constexpr int64_t kLongBwd = 8192;  // more would spill registers
@@ -414,7 +435,7 @@ hipError_t launch_layer_norm_quantize(const NormArgs &a, int dtype, bool pow2, h
 // Enough groups that every compute unit has loads under way, few enough that
 // their sums are little next to dy and x.
 int norm_bwd_groups(int64_t rows, int64_t cols) {
-  const int64_t most = cols <= 1024 ? 4096 : cols <= 4096 ? 1024 : 512;
+  const int64_t most = cols <= 1024 ? 2048 : 512;
   return (int)(rows < most ? rows : most);
 }
 int64_t norm_bwd_row_floats(int64_t rows, int64_t cols) {
@@ -432,7 +453,7 @@ hipError_t launch_layer_norm_backward(const NormBwdArgs &a, int dtype, hipStream
   NormBwdArgs sums = a;
   if (a.rows > 0) sums.partial += norm_bwd_row_floats(a.rows, a.cols);
   return launch(reinterpret_cast<const void *>(&norm_bwd_params_kernel), sums,
-                2 * ((a.cols + 63) / 64), 256, s);
+                2 * ((a.cols + 63) / 64), 64 * kParamWaves, s);
 }
 
 }  // namespace xpose

@@ -37,18 +37,20 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(QuantizeArgs a)
   const int rows = (int)(a.rows - row < 0 ? 0 : a.rows - row > 8 ? 8 : a.rows - row);
   const int cols = (int)(a.cols - col < 0 ? 0 : a.cols - col > 8 ? 8 : a.cols - col);
 
-  float x[8][8];
+  // as they are in memory, and widened at each use: with 16-bit values that
+  // is 32 registers instead of 64, and twice the workgroups on a compute unit
+  Vec8<T> x[8];
   const T *src = (const T *)a.x + row * a.ldx + col;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    load8(src + i * a.ldx, i < rows ? cols : 0, x[i]);
+    x[i] = load_raw8(src + i * a.ldx, i < rows ? cols : 0);
 
   uint32_t row_amax[8], tile_amax = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, magnitude(x[i][j]));
+    for (int j = 0; j < 8; ++j) m = max(m, magnitude(at8<T>(x[i], j)));
     row_amax[i] = m;
     tile_amax = max(tile_amax, m);
   }
@@ -86,18 +88,20 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(QuantizeArgs a)
       a.scale[cb * a.ld_scale + rb] = scale;
       if (BOTH) a.scale_t[rb * a.ld_scale_t + cb] = scale;
     }
-    const Quotient<POW2> by(scale);
+    const Quotient<POW2> by(scale, m);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      float f[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[i][j] = by(x[i][j]);
-      put_row(i, x[i]);
+      for (int j = 0; j < 8; ++j) f[j] = by(at8<T>(x[i], j));
+      put_row(i, f);
     }
     if constexpr (BOTH) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float f[8] = {x[0][j], x[1][j], x[2][j], x[3][j],
-                            x[4][j], x[5][j], x[6][j], x[7][j]};
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = by(at8<T>(x[i], j));
         put_turned(j, f);
       }
     }
@@ -107,7 +111,7 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(QuantizeArgs a)
       for (int j = 0; j < 8; ++j) {
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, magnitude(x[i][j]));
+        for (int i = 0; i < 8; ++i) m = max(m, magnitude(at8<T>(x[i], j)));
         m = max(m, (uint32_t)__shfl_xor((int)m, 16));
         m = max(m, (uint32_t)__shfl_xor((int)m, 32));
         if (t % 64 < 16) col_max[wave][8 * c + j] = m;
@@ -116,12 +120,13 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(QuantizeArgs a)
     float row_scale = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float scale = scale_of<POW2>(max16(row_amax[i]));
+      const uint32_t m = max16(row_amax[i]);
+      const float scale = scale_of<POW2>(m);
       if (c == i) row_scale = scale;
-      const Quotient<POW2> by(scale);
+      const Quotient<POW2> by(scale, m);
       float f[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = by(x[i][j]);
+      for (int j = 0; j < 8; ++j) f[j] = by(at8<T>(x[i], j));
       put_row(i, f);
     }
     // lanes c < 8 of a row group hold its eight scales
@@ -131,13 +136,14 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(QuantizeArgs a)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int at = 8 * c + j;
-        const float scale = scale_of<POW2>(max(max(col_max[0][at], col_max[1][at]),
-                                               max(col_max[2][at], col_max[3][at])));
+        const uint32_t m = max(max(col_max[0][at], col_max[1][at]),
+                               max(col_max[2][at], col_max[3][at]));
+        const float scale = scale_of<POW2>(m);
         if (g == j && j < cols) a.scale_t[rb * a.ld_scale_t + col + j] = scale;
-        const Quotient<POW2> by(scale);
+        const Quotient<POW2> by(scale, m);
         float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = by(x[i][j]);
+        for (int i = 0; i < 8; ++i) f[i] = by(at8<T>(x[i], j));
         put_turned(j, f);
       }
     }
