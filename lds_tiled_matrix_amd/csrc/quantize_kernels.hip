@@ -31,8 +31,13 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(QuantizeArgs a)
   __shared__ uint32_t col_max[4][kTile];
   __shared__ __align__(16) uint8_t turned[BOTH ? kTile * kTile : 16];
   const int t = threadIdx.x, c = t % 16, g = t / 16, wave = t / 64;
-  const int64_t r0 = (int64_t)(blockIdx.x / a.tiles_c) * kTile;
-  const int64_t c0 = (int64_t)(blockIdx.x % a.tiles_c) * kTile;
+  // Workgroups go to the 8 dies in turn: of every 64 tiles a die gets 8
+  // neighbours of a row, which share lines where the pitch is odd, so that
+  // they share a cache too.
+  const uint32_t b = blockIdx.x, run = b / 64 * 64;
+  const uint32_t tile = run + 64 <= gridDim.x ? run + b % 8 * 8 + b / 8 % 8 : b;
+  const int64_t rb = tile / a.tiles_c, cb = tile % a.tiles_c;
+  const int64_t r0 = rb * kTile, c0 = cb * kTile;
   const int64_t row = r0 + 8 * g, col = c0 + 8 * c;
   const int rows = (int)(a.rows - row < 0 ? 0 : a.rows - row > 8 ? 8 : a.rows - row);
   const int cols = (int)(a.cols - col < 0 ? 0 : a.cols - col > 8 ? 8 : a.cols - col);
@@ -56,7 +61,6 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(QuantizeArgs a)
   }
 
   uint8_t *q = a.q + row * a.ldq + col;
-  const int64_t rb = blockIdx.x / a.tiles_c, cb = blockIdx.x % a.tiles_c;
   // The bytes of one row (or column) of the lane's values.
   auto put_row = [&](int i, const float (&f)[8]) {
     if (i >= rows || cols <= 0) return;

@@ -147,9 +147,10 @@ def _vector(t, n: int, dtype, what: str) -> int:
 
 
 def _empty_e4m3(rows: int, cols: int, device):
-    """Uninitialised e4m3 values, rows at multiples of 16 bytes."""
+    """Uninitialised e4m3 values, rows at multiples of 16 bytes, long ones at
+    whole 128-byte lines."""
     import torch
-    pitch = (cols + 15) & ~15
+    pitch = (cols + 15) & ~15 if cols < 1024 else (cols + 127) & ~127
     q = torch.empty((rows, pitch), dtype=torch.float8_e4m3fn, device=device)
     return q if pitch == cols else q[:, :cols]
 
