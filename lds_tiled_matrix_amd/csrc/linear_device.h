@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace xpose {
 namespace {
 
@@ -68,6 +70,15 @@ __device__ inline void store8(T *p, int valid, const float (&f)[8]) {
   }
 }
 
+// f(0) .. f(N - 1), the numbers as constants.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void unrolled(F &&f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    unrolled<N, I + 1>(f);
+  }
+}
+
 // ----- over lanes ------------------------------------------------------------
 
 // x of the lane `N` further on in this lane's row of 16 (cyclic).
@@ -75,6 +86,13 @@ template <int N>
 __device__ inline uint32_t rotate16(uint32_t x) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x120 + N, 0xf, 0xf,
                                                true);
+}
+
+// x of lane N of this lane's row of 16.
+template <int N>
+__device__ inline float from16(float x) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+      0, (int)__float_as_uint(x), 0x150 + N, 0xf, 0xf, true));
 }
 
 // Magnitudes are compared as the integers that their bits are: a NaN is then
@@ -130,6 +148,7 @@ template <bool POW2>
 struct Quotient {
   float up, s, r;
   bool tiny;  // whether any lane of the wave has up != 1 for its sake
+  Quotient() = default;
   __device__ Quotient(float scale, uint32_t amax_bits) {
     if (POW2) {
       r = 1.f / scale;
@@ -141,6 +160,18 @@ struct Quotient {
       s = inf ? 0.f : scale * up;
       r = inf ? 0.f : 1.f / s;
     }
+  }
+  // The divisor that lane N of this lane's row of 16 has.
+  template <int N>
+  __device__ Quotient from() const {
+    Quotient o;
+    o.r = from16<N>(r);
+    if (!POW2) {
+      o.s = from16<N>(s);
+      o.tiny = tiny;
+      if (tiny) o.up = from16<N>(up);
+    }
+    return o;
   }
   __device__ float operator()(float x) const {
     if (POW2) return x * r;

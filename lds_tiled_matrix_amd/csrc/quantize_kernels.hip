@@ -23,6 +23,9 @@ namespace {
 // (16 KiB), in units of 8 rows whose place in a row of the transpose is
 // swizzled by c: writes of 16 lanes (one g, all c) and 16-byte reads then
 // both touch every bank once.
+//
+// Divisions are dear next to the rest (32 a lane made 40% of the instructions):
+// each scale and its reciprocal are worked out once and handed round.
 constexpr int kTile = 128;
 constexpr int kQuantThreads = 256;
 
@@ -30,6 +33,7 @@ template <typename T, int BLOCK_ROWS, bool POW2, bool BOTH>
 __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(QuantizeArgs a) {
   __shared__ uint32_t col_max[4][kTile];
   __shared__ __align__(16) uint8_t turned[BOTH ? kTile * kTile : 16];
+  __shared__ Quotient<POW2> col_by[BOTH && BLOCK_ROWS == 1 ? kTile : 1];
   const int t = threadIdx.x, c = t % 16, g = t / 16, wave = t / 64;
   // Workgroups go to the 8 dies in turn: of every 64 tiles a die gets 8
   // neighbours of a row, which share lines where the pitch is odd, so that
@@ -121,33 +125,39 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(QuantizeArgs a)
         if (t % 64 < 16) col_max[wave][8 * c + j] = m;
       }
     }
-    float row_scale = 0.f;
+    // Lane c < 8 of a row group works out the scale of its row c, for all 16.
+    uint32_t mine = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t m = max16(row_amax[i]);
-      const float scale = scale_of<POW2>(m);
-      if (c == i) row_scale = scale;
-      const Quotient<POW2> by(scale, m);
+      if (c % 8 == i) mine = m;
+    }
+    const float scale = scale_of<POW2>(mine);
+    if (c < rows) a.scale[cb * a.ld_scale + row + c] = scale;
+    const Quotient<POW2> by(scale, mine);
+    unrolled<8>([&](auto i) {
+      const Quotient<POW2> of = by.template from<i>();
       float f[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = by(at8<T>(x[i], j));
+      for (int j = 0; j < 8; ++j) f[j] = of(at8<T>(x[i], j));
       put_row(i, f);
-    }
-    // lanes c < 8 of a row group hold its eight scales
-    if (c < rows) a.scale[cb * a.ld_scale + row + c] = row_scale;
+    });
     if constexpr (BOTH) {
+      // and thread t < 128 that of column t
+      __syncthreads();
+      if (t < kTile) {
+        const uint32_t m = max(max(col_max[0][t], col_max[1][t]), max(col_max[2][t], col_max[3][t]));
+        const float scale = scale_of<POW2>(m);
+        if (c0 + t < a.cols) a.scale_t[rb * a.ld_scale_t + c0 + t] = scale;
+        col_by[t] = Quotient<POW2>(scale, m);
+      }
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int at = 8 * c + j;
-        const uint32_t m = max(max(col_max[0][at], col_max[1][at]),
-                               max(col_max[2][at], col_max[3][at]));
-        const float scale = scale_of<POW2>(m);
-        if (g == j && j < cols) a.scale_t[rb * a.ld_scale_t + col + j] = scale;
-        const Quotient<POW2> by(scale, m);
+        const Quotient<POW2> of = col_by[8 * c + j];
         float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = by(at8<T>(x[i], j));
+        for (int i = 0; i < 8; ++i) f[i] = of(at8<T>(x[i], j));
         put_turned(j, f);
       }
     }
