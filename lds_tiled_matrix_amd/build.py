@@ -1,4 +1,5 @@
-"""Build libxpose.so for gfx950 in-tree.
+"""Build libxpose.so for gfx950 in-tree, and _linear.so, the torch side of
+linear.py, which is host code and built where torch is installed.
 
     python lds_tiled_matrix_amd/build.py
 
@@ -16,6 +17,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libxpose.so")
+TORCH_SOURCE = "linear_torch.cpp"
+TORCH_LIB = os.path.join(HERE, "_linear.so")
 SOURCES = ["xpose_kernels.hip", "xpose_api.cpp", "sgemm_kernels.hip",
            "sgemm_api.cpp", "fp8_gemm_kernels.hip", "quantize_kernels.hip",
            "norm_kernels.hip", "linear_api.cpp"]
@@ -64,7 +67,35 @@ def build(verbose: bool = False) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    build_torch(verbose)
     return LIB
+
+
+def build_torch(verbose: bool = False) -> str | None:
+    """The Python extension over libxpose.so that takes torch tensors."""
+    import importlib.util
+    import sysconfig
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    torch_dir = os.path.dirname(spec.origin)
+    inc = os.path.join(torch_dir, "include")
+    rocm = os.path.dirname(os.path.dirname(hipcc()))
+    tmp = TORCH_LIB + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(rocm, "include"),
+           "-isystem", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, TORCH_SOURCE), "-o", tmp,
+           "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_hip",
+           "-L" + HERE, "-l:libxpose.so", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, TORCH_LIB)
+    return TORCH_LIB
 
 
 def dump_isa(out_dir: str) -> None:
