@@ -129,32 +129,57 @@ __device__ inline void store_run(void *c, int out, int64_t at, int64_t valid, co
   }
 }
 
-__device__ inline void to_lds16(const uint8_t *from, uint8_t *to) {
-  __builtin_amdgcn_global_load_lds(
-      (const __attribute__((address_space(1))) void *)from,
-      (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+// Direct loads to LDS: 16 (4) bytes a lane, from base + offset + step, to
+// `to` and on, lane by lane; zeros where the offset is `bytes` or more.  The
+// buffer descriptor and the step are scalars, so a lane keeps 32 bits of
+// address for all of its loads of a tile.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ inline Buffer buffer(const void *base, int64_t bytes) {
+  const int64_t most = 0xffffffff;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0,
+                                           (int)(uint32_t)(bytes < 0 ? 0 : bytes < most ? bytes : most),
+                                           0x00020000);
 }
-__device__ inline void to_lds4(const float *from, float *to) {
-  __builtin_amdgcn_global_load_lds(
-      (const __attribute__((address_space(1))) void *)from,
-      (__attribute__((address_space(3))) void *)to, 4, 0, 0);
+__device__ inline void to_lds16(Buffer from, uint32_t offset, uint32_t step, void *to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 16,
+                                           (int)offset, (int)step, 0, 0);
+}
+__device__ inline void to_lds4(Buffer from, uint32_t offset, void *to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 4,
+                                           (int)offset, 0, 0, 0);
+}
+
+// Waits until no more than LATER of this wave's loads to LDS are under way (they
+// end in their order) and its reads of LDS are done, then for all waves: what
+// any of them loaded before those, and read, is in place or done with after.
+template <int LATER>
+__device__ inline void loads_and_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(LATER) : "memory");
+}
+// Only the reads: loads stay under way.
+__device__ inline void reads_and_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
 }
 
 // ----- tiles -------------------------------------------------------------------
 //
-// A workgroup has TM x TN outputs, a wave WM x WN of them.  Blocks of 128 k go
-// to LDS by direct 16-byte loads (8 lanes a row), two buffers in turn: the next
-// block's loads are under way while this one is multiplied, one barrier a
-// block.  A row's 8 chunks are permuted by an exclusive or with three bits of
-// the row that differ among the 16 rows of one operand read (of a parity), so
-// that those 16 lanes' 16-byte reads cover all 64 banks.
+// A workgroup has TM x TN outputs, a wave WM x 64 of them.  Blocks of 128 k go
+// to LDS by direct 16-byte loads (8 lanes a row), two buffers in turn.  A row's
+// 8 chunks are permuted by an exclusive or with bits 1 to 3 of its place, so
+// that the 16-byte reads of an operand's 16 rows cover all 64 banks.
+//
+// The matrix cores never wait for LDS: a wave holds the operands of a's rows
+// for a whole block and takes b's 16 rows at a time, the next 16 on the way.
+// Once all waves have a's operands, its half of the buffer begins to be loaded
+// with the block after the next; b's half once they have b's last 16 rows, and
+// then a's operands of the next block come in while the last products use up
+// this one's.  So two barriers a block, and one to one and a half blocks' time
+// for a load to arrive (with one barrier and one block's time, the loads that
+// miss the L2 cache held up every block).
 //
 // b's rows of one operand: lane l has row 16 (l / 4) + 4 j + l % 4 of the
-// wave's 64, so that over j a lane's results are 16 neighbours in c.
-//
-// Scales of a block go to LDS too: of a, a wave's in the order [l][i] (a lane
-// reads its WM / 16 with few wide reads); of b in the rows' order, or for
-// kFp8Pow2 in [l][j].
+// wave's 64, so that over j a lane's results are 16 neighbours in c.  Its place
+// in LDS is 16 j + l.
 template <int TM, int TN, int WM>
 struct Tile {
   static constexpr int WN = 64;
@@ -163,101 +188,117 @@ struct Tile {
   static constexpr int A = 0, B = TM * kBlock, SA = B + TN * kBlock,
                        SB = SA + 4 * TM, BYTES = SB + 4 * TN;
   static_assert(TM + TN <= THREADS && TM % 64 == 0 && TN % 64 == 0);
-  static_assert(TM % (8 * WAVES) == 0 && TN % (8 * WAVES) == 0);
+  static_assert(TM % (8 * WAVES) == 0 && TN % (8 * WAVES) == 0 && (WAVES == 4 || WAVES == 8));
 };
 
-__device__ inline int swizzle_a(int row) { return (row >> 1) & 7; }
-__device__ inline int swizzle_b(int row) { return ((row >> 1) & 1) | ((row >> 3) & 6); }
+__device__ inline int swizzle(int place) { return (place >> 1) & 7; }
+
+// Workgroups go to the 8 dies in turn, and each die has its own L2 cache: it
+// gets one stretch of the tiles, in the order of columns of kGroup tiles, so
+// that what runs on it at one time is nearly square and shares most rows.
+constexpr uint32_t kGroup = 4;
+struct Place {
+  int split;
+  uint32_t tile_m, tile_n;
+};
+__device__ inline Place place(const Fp8GemmArgs &p, uint32_t block, uint32_t grid) {
+  const uint32_t die = block % 8, per = grid / 8, more = grid % 8;
+  uint32_t id = die * per + min(die, more) + block / 8;
+  const uint32_t tiles = p.tiles_m * p.tiles_n;
+  Place at;
+  at.split = (int)(id / tiles);
+  id %= tiles;
+  const uint32_t group = id / (kGroup * p.tiles_n), in = id % (kGroup * p.tiles_n);
+  const uint32_t high = min(kGroup, p.tiles_m - group * kGroup);
+  at.tile_m = group * kGroup + in % high;
+  at.tile_n = in / high;
+  return at;
+}
 
 template <int TM, int TN, int WM, Fp8GemmMode MODE, bool EXACT>
 __global__ __launch_bounds__((Tile<TM, TN, WM>::THREADS)) void fp8_tile_kernel(Fp8GemmArgs p) {
   using T = Tile<TM, TN, WM>;
   __shared__ __align__(16) uint8_t lds[2][T::BYTES];
-  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const int tid = threadIdx.x, lane = tid % 64;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);  // a scalar
   const int l16 = lane % 16, g = lane / 16;
   const int wm = wave % (TM / WM) * WM, wn = wave / (TM / WM) * T::WN;
 
-  uint32_t id = blockIdx.x;
-  const uint32_t tiles = p.tiles_m * p.tiles_n;
-  const int split = (int)(id / tiles);
-  id %= tiles;
-  const int64_t m0 = (int64_t)(id % p.tiles_m) * TM, n0 = (int64_t)(id / p.tiles_m) * TN;
+  int split;
+  int64_t m0, n0;
+  {
+    const Place at = place(p, blockIdx.x, gridDim.x);
+    split = __builtin_amdgcn_readfirstlane(at.split);
+    m0 = (int64_t)at.tile_m * TM;
+    n0 = (int64_t)at.tile_n * TN;
+  }
 
   // this slice's blocks: whole ones from `first` on, and maybe the ragged last
-  const int64_t whole = p.k / kBlock, tail = p.k % kBlock;
-  const int64_t first = (int64_t)split * p.blocks_per_split;
-  int64_t last = first + p.blocks_per_split;
-  const bool ragged = tail && last > whole;
-  if (last > whole) last = whole;
-  const int steps = (int)(last - first) + ragged;
+  const int whole = (int)(p.k / kBlock), tail = (int)(p.k % kBlock);
+  const int first = split * p.blocks_per_split;
+  const int last = min(first + p.blocks_per_split, whole);
+  const bool ragged = tail && first + p.blocks_per_split > whole;
+  const int steps = last - first + ragged;
 
-  // Every load is of a row that exists: rows beyond the matrix are its last
-  // one again, and their results are not stored.
+  // A wave's load covers 8 rows, 16 bytes a lane; the workgroup's, `kRows`.
+  // Rows beyond the matrix come as zeros.
+  constexpr int kRows = 8 * T::WAVES, LA = TM / kRows, LB = TN / kRows;
   const uint8_t *a0 = p.a + m0 * p.lda, *b0 = p.b + n0 * p.ldb;
+  const int64_t bytes_a = (p.m - m0 - 1) * p.lda + p.k, bytes_b = (p.n - n0 - 1) * p.ldb + p.k;
+  const int row_in = wave * 8 + lane / 8;  // of kRows
+  const int at = ((lane % 8) ^ swizzle(row_in)) * 16;
+  const int row_in_b = row_in % 16 / 4 * 16 + row_in / 16 * 4 + row_in % 4;
+  auto first_b = [](int i) { return kRows == 64 ? i * 64 : i / 2 * 64 + i % 2 * 8; };
+  const uint32_t off_a = (uint32_t)row_in * (uint32_t)p.lda + at;
+  const uint32_t off_b = (uint32_t)row_in_b * (uint32_t)p.ldb + at;
   const int rows_a = (int)(p.m - m0 < TM ? p.m - m0 : TM) - 1;
   const int rows_b = (int)(p.n - n0 < TN ? p.n - n0 : TN) - 1;
-  constexpr int LA = TM / (8 * T::WAVES), LB = TN / (8 * T::WAVES);
-  uint32_t off_a[LA], off_b[LB];
-#pragma unroll
-  for (int i = 0; i < LA; ++i) {
-    const int row = (i * T::WAVES + wave) * 8 + lane / 8;
-    off_a[i] = (uint32_t)min(row, rows_a) * (uint32_t)p.lda + ((lane % 8) ^ swizzle_a(row)) * 16;
-  }
-#pragma unroll
-  for (int i = 0; i < LB; ++i) {
-    const int row = (i * T::WAVES + wave) * 8 + lane / 8;
-    off_b[i] = (uint32_t)min(row, rows_b) * (uint32_t)p.ldb + ((lane % 8) ^ swizzle_b(row)) * 16;
-  }
   // The scale that this lane brings to LDS: threads below TM one of a's, the
-  // next TN one of b's.
-  const float *scale = nullptr;
-  int64_t scale_step = 0;
-  if (tid < TM) {
-    const int strip = tid / WM, at = tid % WM;
-    const int row = strip * WM + at % T::NI * 16 + at / T::NI;
-    scale = p.scale_a + m0 + min(row, rows_a);
-    scale_step = p.ld_scale_a;
-  } else if (tid < TM + TN) {
-    int row = tid - TM;
-    if (MODE == kFp8Pow2) {
-      const int l = row % 64 / 4, j = row % 4;
-      row = row / 64 * 64 + l / 4 * 16 + j * 4 + l % 4;
-    }
-    scale = p.scale_b + ((n0 + min(row, rows_b)) >> p.b_shift);
-    scale_step = p.ld_scale_b;
-  }
-
-  auto stage_scales = [&](int64_t kb, uint8_t *buf) {
-    if (tid < TM + TN)  // whole waves
-      to_lds4(scale + kb * scale_step, (float *)(buf + T::SA) + wave * 64);
+  // next TN one of b's; a wave's base and pitch are scalars.
+  const bool scale_of_a = wave < TM / 64;
+  const float *scale0 = scale_of_a ? p.scale_a + m0 : p.scale_b + (n0 >> p.b_shift);
+  const int64_t scale_ld = scale_of_a ? p.ld_scale_a : p.ld_scale_b;
+  const uint32_t off_scale =
+      4 * (scale_of_a ? (uint32_t)min(tid, rows_a)
+                      : (uint32_t)(((n0 + min(tid - TM, rows_b)) >> p.b_shift) - (n0 >> p.b_shift)));
+  auto stage_scales = [&](int kb, uint8_t *buf) {
+    if (TM + TN == T::THREADS || wave < (TM + TN) / 64)
+      to_lds4(buffer(scale0 + kb * scale_ld, 4 * (TM + TN)), off_scale, buf + T::SA + wave * 256);
   };
-  auto stage = [&](int64_t kb, uint8_t *buf) {
-    const uint8_t *a = a0 + kb * kBlock, *b = b0 + kb * kBlock;
+  // Descriptors by the load: rows from the matrix's end on lie past its bytes.
+  Buffer from_a[LA], from_b[LB];
 #pragma unroll
-    for (int i = 0; i < LA; ++i) to_lds16(a + off_a[i], buf + T::A + (i * T::WAVES + wave) * 1024);
+  for (int i = 0; i < LA; ++i) from_a[i] = buffer(a0 + i * kRows * p.lda, bytes_a - i * kRows * p.lda);
 #pragma unroll
-    for (int i = 0; i < LB; ++i) to_lds16(b + off_b[i], buf + T::B + (i * T::WAVES + wave) * 1024);
+  for (int i = 0; i < LB; ++i) from_b[i] = buffer(b0 + first_b(i) * p.ldb, bytes_b - first_b(i) * p.ldb);
+  auto stage_a = [&](int kb, uint8_t *buf) {
+#pragma unroll
+    for (int i = 0; i < LA; ++i)
+      to_lds16(from_a[i], off_a, kb * kBlock, buf + T::A + (i * T::WAVES + wave) * 1024);
+  };
+  auto stage_b = [&](int kb, uint8_t *buf) {
+#pragma unroll
+    for (int i = 0; i < LB; ++i)
+      to_lds16(from_b[i], off_b, kb * kBlock, buf + T::B + (i * T::WAVES + wave) * 1024);
     stage_scales(kb, buf);
   };
   // The last block of k with fewer than 128 columns, the rest as zeros: what
   // lies between k and the pitch may be anything, or no memory at all.
   auto stage_ragged = [&](uint8_t *buf) {
-    const uint8_t *a = a0 + whole * kBlock, *b = b0 + whole * kBlock;
+    const uint8_t *a = a0 + (int64_t)whole * kBlock, *b = b0 + (int64_t)whole * kBlock;
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
-      const int row = (i * T::WAVES + wave) * 8 + lane / 8;
-      const int at = ((lane % 8) ^ swizzle_a(row)) * 16;
+      const int64_t row = min(i * kRows + row_in, rows_a);
       *reinterpret_cast<u32x4 *>(buf + T::A + (i * T::WAVES + wave) * 1024 + lane * 16) =
-          load_chunk(a + off_a[i], tail - at);
+          load_chunk(a + row * p.lda + at, tail - at);
     }
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
-      const int row = (i * T::WAVES + wave) * 8 + lane / 8;
-      const int at = ((lane % 8) ^ swizzle_b(row)) * 16;
+      const int64_t row = min(first_b(i) + row_in_b, rows_b);
       *reinterpret_cast<u32x4 *>(buf + T::B + (i * T::WAVES + wave) * 1024 + lane * 16) =
-          load_chunk(b + off_b[i], tail - at);
+          load_chunk(b + row * p.ldb + at, tail - at);
     }
-    stage_scales(whole, buf);
+    stage_scales((int)whole, buf);
   };
 
   f32x4 acc[T::NI][T::NJ];
@@ -266,63 +307,106 @@ __global__ __launch_bounds__((Tile<TM, TN, WM>::THREADS)) void fp8_tile_kernel(F
 #pragma unroll
     for (int j = 0; j < T::NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int row_b = wn + l16 / 4 * 16 + l16 % 4;  // + 4 j
-  auto chunk = [&](const uint8_t *base, int row, int swizzle) {
-    const u32x4 *r = reinterpret_cast<const u32x4 *>(base + row * kBlock);
-    Lane32<EXACT> v;
-    v.set(r[g ^ swizzle], r[(g + 4) ^ swizzle]);
+  // One operand read from LDS: 32 bytes, and the scales that go with them.
+  struct Rows16 {
+    u32x4 lo, hi;
+    float scale;  // of the lane's row (kFp8Rows: not b's)
+    f32x4 scales; // kFp8Rows: of the four rows of b whose results the lane has
+  };
+  // A lane's places, from a buffer's start and for i = j = 0: the others lie at
+  // constant distances, which the reads hold themselves.
+  const int x = swizzle(l16), lo = (g ^ x) * 16, hi = ((g + 4) ^ x) * 16;
+  const int place_a = T::A + (wm + l16) * kBlock, place_b = T::B + (wn + l16) * kBlock;
+  const int place_sa = T::SA + 4 * (wm + l16);
+  const int place_sb = T::SB + 4 * (MODE == kFp8Pow2   ? wn + l16 / 4 * 16 + l16 % 4
+                                    : MODE == kFp8Rows ? wn + 16 * g
+                                                       : wn);  // 64 rows of one tile
+  auto read_a = [&](const uint8_t *buf, int i) {
+    Rows16 v;
+    v.lo = *reinterpret_cast<const u32x4 *>(buf + (place_a + lo) + i * 16 * kBlock);
+    v.hi = *reinterpret_cast<const u32x4 *>(buf + (place_a + hi) + i * 16 * kBlock);
+    v.scale = *reinterpret_cast<const float *>(buf + place_sa + i * 64);
     return v;
   };
-  auto compute = [&](const uint8_t *buf) {
-    const float *sa = (const float *)(buf + T::SA) + wm + l16 * T::NI;
-    const float *sb = (const float *)(buf + T::SB) + wn;
-    Lane32<EXACT> b[T::NJ];
-#pragma unroll
-    for (int j = 0; j < T::NJ; ++j) b[j] = chunk(buf + T::B, row_b + 4 * j, swizzle_b(row_b + 4 * j));
-    f32x4 sbj[T::NJ];
-    int eb[T::NJ];
-    float sb1 = 0.f;
-    if constexpr (MODE == kFp8Pow2) {
-#pragma unroll
-      for (int j = 0; j < T::NJ; ++j) eb[j] = exponent_of(sb[l16 * 4 + j]);
-    } else if constexpr (MODE == kFp8Rows) {
-#pragma unroll
-      for (int j = 0; j < T::NJ; ++j) sbj[j] = *reinterpret_cast<const f32x4 *>(sb + g * 16 + 4 * j);
-    } else {
-      sb1 = sb[0];  // 64 columns of one 128-block
-    }
-#pragma unroll
-    for (int i = 0; i < T::NI; ++i) {
-      const int row = wm + 16 * i + l16;
-      const Lane32<EXACT> a = chunk(buf + T::A, row, swizzle_a(row));
-      if constexpr (MODE == kFp8Pow2) {
-        const int ea = exponent_of(sa[i]);
-#pragma unroll
-        for (int j = 0; j < T::NJ; ++j) acc[i][j] = multiply(b[j], a, acc[i][j], eb[j], ea);
-      } else {
-        const float s1 = MODE == kFp8Tiles ? sa[i] * sb1 : sa[i];
-#pragma unroll
-        for (int j = 0; j < T::NJ; ++j) {
-          const f32x4 v = multiply(b[j], a);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[i][j][e] = __builtin_fmaf(v[e], MODE == kFp8Rows ? s1 * sbj[j][e] : s1, acc[i][j][e]);
-        }
-      }
-    }
+  auto read_b = [&](const uint8_t *buf, int j) {
+    Rows16 v;
+    v.lo = *reinterpret_cast<const u32x4 *>(buf + (place_b + lo) + j * 16 * kBlock);
+    v.hi = *reinterpret_cast<const u32x4 *>(buf + (place_b + hi) + j * 16 * kBlock);
+    if constexpr (MODE == kFp8Pow2) v.scale = *reinterpret_cast<const float *>(buf + place_sb + j * 16);
+    if constexpr (MODE == kFp8Tiles) v.scale = *reinterpret_cast<const float *>(buf + place_sb);
+    if constexpr (MODE == kFp8Rows) v.scales = *reinterpret_cast<const f32x4 *>(buf + place_sb + j * 16);
+    return v;
   };
 
   // The ragged block goes first: nothing is under way yet that its loads
   // through registers would hold up.
   if (steps > 0) {
-    if (ragged) stage_ragged(lds[0]); else stage(first, lds[0]);
+    if (ragged) {
+      stage_ragged(lds[0]);
+    } else {
+      stage_a(first, lds[0]);
+      stage_b(first, lds[0]);
+    }
   }
-  __syncthreads();
-  for (int s = 0; s < steps; ++s) {
-    if (s + 1 < steps) stage(first + s + 1 - ragged, lds[(s + 1) & 1]);
-    compute(lds[s & 1]);
-    __syncthreads();
+  loads_and_barrier<0>();
+  if (steps > 1) {
+    stage_a(first + 1 - ragged, lds[1]);
+    stage_b(first + 1 - ragged, lds[1]);
   }
+  Rows16 a[T::NI], b = read_b(lds[0], 0);
+#pragma unroll
+  for (int i = 0; i < T::NI; ++i) a[i] = read_a(lds[0], i);
+  // One block.  MORE: there is a next one; STAGE: and one after that.  These
+  // are constants so that a block is one stretch of code, without branches for
+  // products to be moved across.
+  auto block = [&](int s, auto stage_next, auto more) {
+    constexpr bool STAGE = stage_next(), MORE = more();
+    uint8_t *const buf = lds[s & 1], *const next = lds[(s + 1) & 1];
+    Lane32<EXACT> al[T::NI];
+#pragma unroll
+    for (int i = 0; i < T::NI; ++i) al[i].set(a[i].lo, a[i].hi);
+#pragma unroll
+    for (int j = 0; j < T::NJ; ++j) {
+      const Rows16 now = b;
+      Lane32<EXACT> bl;
+      bl.set(now.lo, now.hi);
+      if (j + 1 < T::NJ) {
+        b = read_b(buf, j + 1);
+      } else if constexpr (MORE) {
+        // every wave has all of this block, and the next has landed
+        loads_and_barrier<STAGE ? LA : 0>();
+        if constexpr (STAGE) stage_b(first + s + 2 - ragged, buf);
+        b = read_b(next, 0);
+      }
+      if (STAGE && j == 1) {
+        reads_and_barrier();  // every wave has a's operands of this block
+        stage_a(first + s + 2 - ragged, buf);
+      }
+#pragma unroll
+      for (int i = 0; i < T::NI; ++i) {
+        if constexpr (MODE == kFp8Pow2) {
+          acc[i][j] = multiply(bl, al[i], acc[i][j], exponent_of(now.scale), exponent_of(a[i].scale));
+        } else {
+          const f32x4 v = multiply(bl, al[i]);
+          const float s1 = MODE == kFp8Tiles ? a[i].scale * now.scale : a[i].scale;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[i][j][e] = __builtin_fmaf(v[e], MODE == kFp8Rows ? s1 * now.scales[e] : s1, acc[i][j][e]);
+        }
+        if (MORE && j + 1 == T::NJ) {
+          // in this order: the registers of a[i] are free from here on
+          __builtin_amdgcn_sched_barrier(0);
+          a[i] = read_a(next, i);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  using std::bool_constant;
+  int s = 0;
+  for (; s + 2 < steps; ++s) block(s, bool_constant<true>{}, bool_constant<true>{});
+  if (s + 1 < steps) block(s++, bool_constant<false>{}, bool_constant<true>{});
+  if (s < steps) block(s, bool_constant<false>{}, bool_constant<false>{});
 
   uint8_t *c = (uint8_t *)p.c + (int64_t)split * p.slice * 4;  // slices are float32
   const int64_t col = n0 + wn + 16 * g;
