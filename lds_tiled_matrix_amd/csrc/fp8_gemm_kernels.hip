@@ -362,6 +362,13 @@ __global__ __launch_bounds__((Tile<TM, TN, WM>::THREADS)) void fp8_tile_kernel(F
   auto block = [&](int s, auto stage_next, auto more) {
     constexpr bool STAGE = stage_next(), MORE = more();
     uint8_t *const buf = lds[s & 1], *const next = lds[(s + 1) & 1];
+    f32x4 last, last_s2;
+    float last_s1;
+    auto add = [&](f32x4 &sum) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        sum[e] = __builtin_fmaf(last[e], MODE == kFp8Rows ? last_s1 * last_s2[e] : last_s1, sum[e]);
+    };
     Lane32<EXACT> al[T::NI];
 #pragma unroll
     for (int i = 0; i < T::NI; ++i) al[i].set(a[i].lo, a[i].hi);
@@ -387,11 +394,13 @@ __global__ __launch_bounds__((Tile<TM, TN, WM>::THREADS)) void fp8_tile_kernel(F
         if constexpr (MODE == kFp8Pow2) {
           acc[i][j] = multiply(bl, al[i], acc[i][j], exponent_of(now.scale), exponent_of(a[i].scale));
         } else {
+          // Each product is added in behind the next one's start, not waited for.
           const f32x4 v = multiply(bl, al[i]);
-          const float s1 = MODE == kFp8Tiles ? a[i].scale * now.scale : a[i].scale;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[i][j][e] = __builtin_fmaf(v[e], MODE == kFp8Rows ? s1 * now.scales[e] : s1, acc[i][j][e]);
+          if (i > 0) add(acc[i - 1][j]);
+          else if (j > 0) add(acc[T::NI - 1][j - 1]);
+          last = v;
+          last_s1 = MODE == kFp8Tiles ? a[i].scale * now.scale : a[i].scale;
+          last_s2 = now.scales;
         }
         if (MORE && j + 1 == T::NJ) {
           // in this order: the registers of a[i] are free from here on
@@ -401,6 +410,7 @@ __global__ __launch_bounds__((Tile<TM, TN, WM>::THREADS)) void fp8_tile_kernel(F
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    if constexpr (MODE != kFp8Pow2) add(acc[T::NI - 1][T::NJ - 1]);
   };
   using std::bool_constant;
   int s = 0;
