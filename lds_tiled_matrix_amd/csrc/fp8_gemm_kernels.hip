@@ -92,6 +92,7 @@ __device__ inline f32x4 multiply(const Lane32<false> &b, const Lane32<false> &a,
 __device__ inline u32x4 load_chunk(const uint8_t *p, int64_t valid) {
   if (valid >= 16) return *reinterpret_cast<const u32x4 *>(p);
   u32x4 w = {0, 0, 0, 0};
+  if (valid <= 0) return w;
 #pragma unroll
   for (int e = 0; e < 16; ++e)
     if (e < valid) w[e / 4] |= (uint32_t)p[e] << (8 * (e % 4));
@@ -216,7 +217,7 @@ __device__ inline Place place(const Fp8GemmArgs &p, uint32_t block, uint32_t gri
 }
 
 template <int TM, int TN, int WM, Fp8GemmMode MODE, bool EXACT>
-__global__ __launch_bounds__((Tile<TM, TN, WM>::THREADS)) void fp8_tile_kernel(Fp8GemmArgs p) {
+__global__ __launch_bounds__((Tile<TM, TN, WM>::THREADS), 2) void fp8_tile_kernel(Fp8GemmArgs p) {
   using T = Tile<TM, TN, WM>;
   __shared__ __align__(16) uint8_t lds[2][T::BYTES];
   const int tid = threadIdx.x, lane = tid % 64;
@@ -449,13 +450,13 @@ hipError_t launch_tile(const Fp8GemmArgs &a, Fp8GemmMode mode, hipStream_t s) {
 //
 // Serving: reading b bounds it.  A workgroup has 16 rows of b and up to 16 MS
 // of a; its waves take the blocks of k in turn, straight from memory into the
-// instruction's registers, four at a time, and their sums are added through
+// instruction's registers, two or four at a time, and their sums are added through
 // LDS in the waves' order.
 constexpr int kSkinnyWaves = 8;
 
 template <int MS, bool EXACT>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void fp8_skinny_kernel(Fp8GemmArgs p) {
-  constexpr int kDepth = MS > 2 ? 2 : 4;
+  constexpr int kDepth = MS > 1 ? 2 : 4;
   __shared__ __align__(16) float sums[kSkinnyWaves][MS][64][4];
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
   const int l16 = lane % 16, g = lane / 16;

@@ -94,45 +94,76 @@ struct GemmPlan {
   int64_t workspace = 0;
 };
 
-constexpr int64_t kUnits = 256;  // compute units
 constexpr int64_t kMaxSplits = 16;
 
-const xpose::Fp8GemmKernel *gemm_kernel(int tile_m, bool skinny, bool exact) {
-  int count = 0;
-  const xpose::Fp8GemmKernel *table = xpose::fp8_gemm_kernels(&count);
-  for (int i = 0; i < count; ++i)
-    if (table[i].tile_m == tile_m && table[i].skinny == skinny && table[i].exact == exact)
-      return &table[i];
-  return nullptr;
+// Estimated microseconds of a product on MI355X, for choosing among kernels.
+// Fitted to 96 shapes from 48 x 64 x 128 to 2048 x 4096 x 8192, bfloat16 and
+// float32 results, each with every kernel and 1 to 16 slices; the choice was
+// within 10% of the fastest for all but a few, 25% at worst.
+//
+// Tiles: a start, then a block of k takes `one` while the compute units hold a
+// workgroup each and `two` with two of the 128 x 128 tiles on each (of 256 x
+// 256 only one fits); a lone workgroup waits for memory, so that the second
+// costs the 8-bit kernels half as much again and the exact ones, which the
+// matrix cores and conversions bound, all of it.  Slices are written and read
+// as float32 by a launch of its own.
+double tile_time(const xpose::Fp8GemmKernel &kern, int64_t tiles, int64_t splits,
+                 int64_t blocks, double outputs, int out_size) {
+  const bool large = kern.tile_m == 256;
+  const double one = large ? 1.75 : kern.exact ? 1.2 : 0.85;
+  const double two = large ? 3.5 : kern.exact ? 2.1 : 1.25;
+  const int64_t groups = tiles * splits, rest = groups % 512;
+  const double rounds = (double)(groups / 512) * two + (rest > 256 ? two : rest ? one : 0);
+  double t = (large ? 5.0 : 3.3) + rounds * (double)ceil_div(blocks, splits) +
+             outputs * out_size / 4e6;
+  if (splits > 1) t += 2.2 + outputs * (8.0 * splits + out_size) / 3e6;
+  return t;
+}
+
+// Few rows: rounds of the workgroups that fit at once; a block of k costs more
+// where it is not among the first 16, which are on their way together, and with
+// more rows of a to read for it.
+double skinny_time(const xpose::Fp8GemmKernel &kern, int64_t groups, int64_t blocks) {
+  const bool wide = kern.tile_m == 64;
+  const int64_t at_once = wide ? 256 : 512;
+  const double first = wide ? 0.17 : kern.tile_m == 32 ? 0.12 : 0.04;
+  const double later = wide ? 0.25 : kern.tile_m == 32 ? 0.165 : 0.085;
+  const double b = (double)std::min<int64_t>(blocks, 16), more = (double)blocks - b;
+  return 0.8 + (double)ceil_div(groups, at_once) * ((wide ? 2.9 : 2.5) + first * b + later * more);
 }
 
 int plan_gemm(int64_t m, int64_t n, int64_t k, int out_dtype, GemmPlan &plan) {
   const bool exact = out_dtype == XPOSE_F32;
-  const int64_t blocks = ceil_div(k, kBlock);
-  int64_t want = 1;
-  if (m <= 64) {
-    plan.kernel = gemm_kernel(m <= 16 ? 16 : m <= 32 ? 32 : 64, true, exact);
-  } else {
-    const int64_t big = ceil_div(m, 256) * ceil_div(n, 256);
-    plan.kernel = gemm_kernel(big >= 160 && !exact ? 256 : 128, false, exact);
+  const int64_t blocks = std::max<int64_t>(1, ceil_div(k, kBlock));
+  const double outputs = (double)m * (double)n;
+  const int skinny_rows = m <= 16 ? 16 : m <= 32 ? 32 : 64;
+  int count = 0;
+  const xpose::Fp8GemmKernel *table = xpose::fp8_gemm_kernels(&count);
+  double best = 0;
+  for (int i = 0; i < count; ++i) {
+    const xpose::Fp8GemmKernel &kern = table[i];
+    if (kern.exact != exact || (kern.skinny && kern.tile_m != skinny_rows)) continue;
+    const int64_t tiles_m = ceil_div(m, kern.tile_m), tiles_n = ceil_div(n, kern.tile_n);
+    int64_t tiles;
+    if (__builtin_mul_overflow(tiles_m, tiles_n, &tiles) || tiles > kMaxGrid / kMaxSplits)
+      continue;
+    const int64_t most = kern.skinny || kern.tile_m == 256 ? 1 : kMaxSplits;
+    for (int64_t want = 1; want <= most && want <= blocks; ++want) {
+      const int64_t per = ceil_div(blocks, want), splits = ceil_div(blocks, per);
+      if (splits != want) continue;
+      int64_t bytes = 0;
+      if (splits > 1 && (__builtin_mul_overflow(m, n, &bytes) ||
+                         __builtin_mul_overflow(bytes, 4 * splits, &bytes)))
+        continue;
+      const double t = kern.skinny ? skinny_time(kern, tiles, blocks)
+                                   : tile_time(kern, tiles, splits, blocks, outputs, exact ? 4 : 2);
+      if (!plan.kernel || t < best) {
+        best = t;
+        plan = GemmPlan{&kern, tiles_m, tiles_n, per, splits, bytes};
+      }
+    }
   }
-  plan.tiles_m = ceil_div(m, plan.kernel->tile_m);
-  plan.tiles_n = ceil_div(n, plan.kernel->tile_n);
-  int64_t tiles;
-  if (__builtin_mul_overflow(plan.tiles_m, plan.tiles_n, &tiles) || tiles > kMaxGrid / kMaxSplits)
-    return XPOSE_EINVAL;
-  if (!plan.kernel->skinny && plan.kernel->tile_m == 128)
-    want = std::max<int64_t>(1, std::min({2 * kUnits / tiles, blocks / 4, kMaxSplits}));
-  plan.blocks_per_split = std::max<int64_t>(1, ceil_div(blocks, want));
-  plan.splits = std::max<int64_t>(1, ceil_div(blocks, plan.blocks_per_split));
-  if (plan.splits > 1) {
-    int64_t bytes;
-    if (__builtin_mul_overflow(m, n, &bytes) ||
-        __builtin_mul_overflow(bytes, 4 * plan.splits, &bytes))
-      return XPOSE_EINVAL;
-    plan.workspace = bytes;
-  }
-  return XPOSE_OK;
+  return plan.kernel ? XPOSE_OK : XPOSE_EINVAL;
 }
 
 int check_gemm(int64_t m, int64_t n, int64_t k, int32_t b_block_rows,

@@ -105,8 +105,8 @@ def test_gemm(m, n, k, block_rows, pow2):
 
 
 @pytest.mark.parametrize("m,n,k,block_rows,pow2", [
-    (2048, 5000, 400, 128, False), (2048, 5200, 400, 1, False), (2304, 5000, 400, 128, True),
-    (2500, 4900, 130, 1, True)])
+    (4000, 4090, 400, 128, False), (3850, 4096, 400, 1, False), (4096, 3999, 400, 128, True),
+    (3901, 4090, 300, 1, True), (4000, 4090, 384, 1, False)])
 def test_gemm_large_tiles(m, n, k, block_rows, pow2):
     """Enough tiles of 256 x 256 for those to be taken, with ragged edges."""
     assert X.fp8_gemm_plan(m, n, k, block_rows=block_rows)["tile_m"] == 256
@@ -133,9 +133,10 @@ def test_gemm_is_exact_on_small_integers(m, n, k, block_rows, pow2):
 
 
 def test_gemm_splits_of_k_and_their_sum():
-    info = X.fp8_gemm_plan(300, 500, 4096)
+    info = X.fp8_gemm_plan(300, 500, 8200, out_dtype=F32)
     assert info["splits"] > 1
-    ops = _operands(300, 500, 4096, 1, False, 3)
+    test_gemm(300, 500, 8200, 1, False)
+    ops = _operands(300, 500, 8200, 1, False, 3)
     first = _gemm(*ops, F32, False)
     for _ in range(3):
         assert torch.equal(first, _gemm(*ops, F32, False))
