@@ -70,6 +70,26 @@ __device__ inline void store8(T *p, int valid, const float (&f)[8]) {
   }
 }
 
+// The same where the values will not be read again soon: past the caches.
+template <typename T>
+__device__ inline void store8_past(T *p, int valid, const float (&f)[8]) {
+  if (valid < 8) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < valid) p[e] = (T)f[e];
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      __builtin_nontemporal_store(f32x4_any{f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]},
+                                  reinterpret_cast<f32x4_any *>(p) + h);
+  } else {
+    decltype(Vec8<T>::v) r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = (T)f[e];
+    __builtin_nontemporal_store(r, reinterpret_cast<decltype(r) *>(p));
+  }
+}
+
 // f(0) .. f(N - 1), the numbers as constants.
 template <int N, int I = 0, typename F>
 __device__ __forceinline__ void unrolled(F &&f) {

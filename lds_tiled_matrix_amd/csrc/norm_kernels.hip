@@ -38,7 +38,8 @@ __device__ inline int in_row(int64_t cols, int64_t col) {
 
 // Sums over the lanes of a row, the same in all of them.  With one wave a row
 // no LDS is needed; else `lds` holds a float for each wave, and two calls in
-// turn use two of them, so that one barrier a call is enough.
+// turn use two of them, so that one barrier a call is enough: who writes to the
+// first one again has passed the second's barrier, behind everybody's reads.
 template <int TR>
 __device__ inline float row_sum(float x, float *lds) {
   x = sum64(x);
@@ -85,50 +86,68 @@ __device__ inline void put_chunk(const NormArgs &a, int64_t row, int64_t col, in
 
 constexpr int norm_threads(int tr) { return tr == 64 ? 256 : tr; }
 
+// Workgroups stay: a group of TR lanes walks over rows `groups` apart with the
+// weight and bias in registers (read anew for each row they are four times a
+// bfloat16 row's bytes: 8192 x 8192 took 56 us so), and the next row's loads
+// are under way while this one is worked on.
 template <typename T, Out OUT, int TR, int NC>
 __global__ __launch_bounds__(norm_threads(TR)) void norm_kernel(NormArgs a) {
   __shared__ float lds[2][TR > 64 ? TR / 64 : 1];
   const int lane = threadIdx.x % TR;
-  const int64_t row = (int64_t)blockIdx.x * (norm_threads(TR) / TR) + threadIdx.x / TR;
-  if (row >= a.rows) return;  // whole waves, and none where barriers follow
-  const T *x = (const T *)a.x + row * a.ldx;
-  float v[NC][8];
-  float s = 0.f;
+  const int64_t first = (int64_t)blockIdx.x * (norm_threads(TR) / TR) + threadIdx.x / TR;
+  const int64_t groups = (int64_t)gridDim.x * (norm_threads(TR) / TR);
+  if (first >= a.rows) return;  // whole waves, and none where barriers follow
+  float w[NC][8], b[NC][8];
+  Vec8<T> ahead[NC];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int64_t col = (i * TR + lane) * 8;
-    load8(x + col, in_row(a.cols, col), v[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < NC; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s += v[i][e];
-  const float mean = row_sum<TR>(s, lds[0]) / (float)a.cols;
-  s = 0.f;
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int valid = in_row(a.cols, (i * TR + lane) * 8);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      v[i][e] = e < valid ? v[i][e] - mean : 0.f;
-      s = __builtin_fmaf(v[i][e], v[i][e], s);
+    for (int i = 0; i < NC; ++i) {
+      const int64_t col = (i * TR + lane) * 8;
+      ahead[i] = load_raw8((const T *)a.x + row * a.ldx + col, in_row(a.cols, col));
     }
-  }
-  const float rstd = 1.f / sqrtf(row_sum<TR>(s, lds[1]) / (float)a.cols + a.eps);
-  if (lane == 0 && a.mean) {
-    a.mean[row] = mean;
-    a.rstd[row] = rstd;
-  }
+  };
+  fetch(first);
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int64_t col = (i * TR + lane) * 8;
-    const int valid = in_row(a.cols, col);
-    float w[8], b[8], y[8];
-    load_param8(a.weight, a.param_dtype, col, valid, 1.f, w);
-    load_param8(a.bias, a.param_dtype, col, valid, 0.f, b);
+    load_param8(a.weight, a.param_dtype, col, in_row(a.cols, col), 1.f, w[i]);
+    load_param8(a.bias, a.param_dtype, col, in_row(a.cols, col), 0.f, b[i]);
+  }
+  for (int64_t row = first; row < a.rows; row += groups) {
+    float v[NC][8];
+    float s = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(v[i][e] * rstd, w[e], b[e]);
-    put_chunk<T, OUT>(a, row, col, valid, y);
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[i][e] = at8<T>(ahead[i], e);
+        s += v[i][e];
+      }
+    if (row + groups < a.rows) fetch(row + groups);
+    const float mean = row_sum<TR>(s, lds[0]) / (float)a.cols;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int valid = in_row(a.cols, (i * TR + lane) * 8);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[i][e] = e < valid ? v[i][e] - mean : 0.f;
+        s = __builtin_fmaf(v[i][e], v[i][e], s);
+      }
+    }
+    const float rstd = 1.f / sqrtf(row_sum<TR>(s, lds[1]) / (float)a.cols + a.eps);
+    if (lane == 0 && a.mean) {
+      a.mean[row] = mean;
+      a.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int64_t col = (i * TR + lane) * 8;
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(v[i][e] * rstd, w[i][e], b[i][e]);
+      put_chunk<T, OUT>(a, row, col, in_row(a.cols, col), y);
+    }
   }
 }
 
@@ -190,9 +209,11 @@ hipError_t launch(const void *kernel, const NormArgs &a, uint32_t grid, int thre
 }
 template <typename T, Out OUT, int TR, int NC>
 hipError_t launch_norm(const NormArgs &a, hipStream_t s) {
-  constexpr int per = norm_threads(TR) / TR;
+  // as many workgroups as the registers let run at once, or a few more
+  constexpr int per = norm_threads(TR) / TR, most = 256 * (TR <= 256 ? 6 : TR == 512 ? 3 : 2);
+  const int64_t grid = (a.rows + per - 1) / per;
   return launch(reinterpret_cast<const void *>(&norm_kernel<T, OUT, TR, NC>), a,
-                (uint32_t)((a.rows + per - 1) / per), norm_threads(TR), s);
+                (uint32_t)(grid < most ? grid : most), norm_threads(TR), s);
 }
 template <typename T, Out OUT>
 hipError_t norm(const NormArgs &a, hipStream_t s) {

@@ -218,7 +218,9 @@ hipError_t quantize(const QuantizeArgs &a, int block_rows, bool pow2, hipStream_
 // from the L2 cache) and scales its chunks.  Squares and sums are of 64 bits:
 // no square overflows, and the sum of 10^9 gradients loses nothing; their
 // cost hides behind the loads.  The second launch walks backwards, so that it
-// begins with what the first one left in the caches.
+// begins with what the first one left in the caches, and stores past them, so
+// that this stays there (32 layers' gradients, 760 MB in bfloat16: 383 us
+// without, 348 us with).
 constexpr int kClipThreads = 256;
 
 struct Span {
@@ -284,7 +286,7 @@ __device__ inline void scale_span(const T *in, T *out, int64_t count, float fact
     load8(in + i, valid, f);
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] *= factor;
-    store8(out + i, valid, f);
+    store8_past(out + i, valid, f);
   }
 }
 
