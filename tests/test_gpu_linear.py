@@ -590,3 +590,44 @@ def test_refusals():
     ]:
         with pytest.raises(error):
             call()
+
+
+# ----- the layer of examples/fp8_linear.py ------------------------------------------------------
+
+def _example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "fp8_linear.py")
+    spec = importlib.util.spec_from_file_location("fp8_linear_example", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+@pytest.mark.parametrize("tokens,width,outputs", [(700, 333, 200), (1000, 1024, 640)])
+def test_layer_gradients(tokens, width, outputs):
+    """The whole step against float64 autograd of the unquantised layer: e4m3
+    keeps each operand within 2^-4 of itself, so each product within 2^-3 of
+    its magnitudes and far nearer in the norm of the whole."""
+    ex = _example()
+    layer = ex.Fp8Linear(width, outputs, _dev(), seed=4)
+    layer.gain += 0.1 * torch.randn(width, device=_dev())
+    layer.bias += 0.1 * torch.randn(width, device=_dev())
+    x = (torch.randn(tokens, width, device=_dev()) + 0.3).bfloat16()
+    grad = (torch.randn(tokens, outputs, device=_dev()) * 1e-2).bfloat16()
+    wq = layer.quantized_weight()
+    out, saved = layer.forward(x, wq)
+    gx, grads = layer.backward(grad, saved, wq)
+    ref = [t.double().cpu().requires_grad_() for t in (x, *layer.parameters())]
+    y = torch.nn.functional.layer_norm(ref[0], (width,), ref[1], ref[2], 1e-5) @ ref[3].t()
+    y.backward(grad.double().cpu())
+    for got, want in zip([out, gx, *grads], [y.detach()] + [r.grad for r in ref]):
+        off = (got.double().cpu() - want).norm() / want.norm()
+        assert off < 2.0 ** -3, off
+    served = layer.serve(x[:3], wq)
+    assert (served.double().cpu() - y.detach()[:3]).norm() / y.detach()[:3].norm() < 2.0 ** -3
+
+
+def test_training_learns():
+    losses = _example().train(tokens=512, width=256, outputs=192, steps=12, log=None)
+    assert losses[-1] < 0.5 * losses[0]
