@@ -97,26 +97,26 @@ struct GemmPlan {
 constexpr int64_t kMaxSplits = 16;
 
 // Estimated microseconds of a product on MI355X, for choosing among kernels.
-// Fitted to 96 shapes from 48 x 64 x 128 to 2048 x 4096 x 8192, bfloat16 and
-// float32 results, each with every kernel and 1 to 16 slices; the choice was
-// within 10% of the fastest for all but a few, 25% at worst.
+// Fitted to 160 shapes from 1 x 64 x 128 to 5000 x 4096 x 8192, with bfloat16
+// and with float32 results, each timed with every kernel and 1 to 16 slices:
+// the choice is within 10% of the fastest for all but two of them, 15% at
+// worst.
 //
 // Tiles: a start, then a block of k takes `one` while the compute units hold a
 // workgroup each and `two` with two of the 128 x 128 tiles on each (of 256 x
 // 256 only one fits); a lone workgroup waits for memory, so that the second
-// costs the 8-bit kernels half as much again and the exact ones, which the
-// matrix cores and conversions bound, all of it.  Slices are written and read
-// as float32 by a launch of its own.
+// costs about half as much again.  Slices are written and read as float32 by a
+// launch of its own.
 double tile_time(const xpose::Fp8GemmKernel &kern, int64_t tiles, int64_t splits,
                  int64_t blocks, double outputs, int out_size) {
   const bool large = kern.tile_m == 256;
-  const double one = large ? 1.75 : kern.exact ? 1.2 : 0.85;
-  const double two = large ? 3.5 : kern.exact ? 2.1 : 1.25;
+  const double one = large ? 1.75 : kern.exact ? 1.2 : 0.8;
+  const double two = large ? 3.5 : kern.exact ? 1.75 : 1.15;
   const int64_t groups = tiles * splits, rest = groups % 512;
   const double rounds = (double)(groups / 512) * two + (rest > 256 ? two : rest ? one : 0);
   double t = (large ? 5.0 : 3.3) + rounds * (double)ceil_div(blocks, splits) +
              outputs * out_size / 4e6;
-  if (splits > 1) t += 2.2 + outputs * (8.0 * splits + out_size) / 3e6;
+  if (splits > 1) t += 2.2 + outputs * (8.0 * splits + out_size) / 4e6;
   return t;
 }
 
