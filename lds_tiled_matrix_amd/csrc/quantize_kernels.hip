@@ -33,7 +33,8 @@ template <typename T, int BLOCK_ROWS, bool POW2, bool BOTH>
 __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(QuantizeArgs a) {
   __shared__ uint32_t col_max[4][kTile];
   __shared__ __align__(16) uint8_t turned[BOTH ? kTile * kTile : 16];
-  __shared__ Quotient<POW2> col_by[BOTH && BLOCK_ROWS == 1 ? kTile : 1];
+  // of column 8 c + j at [j][c]: lanes next to each other read neighbours
+  __shared__ Quotient<POW2> col_by[8][BOTH && BLOCK_ROWS == 1 ? 16 : 1];
   const int t = threadIdx.x, c = t % 16, g = t / 16, wave = t / 64;
   // Workgroups go to the 8 dies in turn: of every 64 tiles a die gets 8
   // neighbours of a row, which share lines where the pitch is odd, so that
@@ -152,12 +153,12 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(QuantizeArgs a)
         const uint32_t m = max(max(col_max[0][t], col_max[1][t]), max(col_max[2][t], col_max[3][t]));
         const float scale = scale_of<POW2>(m);
         if (c0 + t < a.cols) a.scale_t[rb * a.ld_scale_t + c0 + t] = scale;
-        col_by[t] = Quotient<POW2>(scale, m);
+        col_by[t % 8][t / 8] = Quotient<POW2>(scale, m);
       }
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const Quotient<POW2> of = col_by[8 * c + j];
+        const Quotient<POW2> of = col_by[j][c];
         float f[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = of(at8<T>(x[i], j));
