@@ -89,7 +89,7 @@ constexpr int norm_threads(int tr) { return tr == 64 ? 256 : tr; }
 // Workgroups stay: a group of TR lanes walks over rows `groups` apart with the
 // weight and bias in registers (read anew for each row they are four times a
 // bfloat16 row's bytes: 8192 x 8192 took 56 us so), and the next row's loads
-// are under way while this one is worked on.
+// are under way while this one is worked on: 45 us, 6.0 TB/s.
 template <typename T, Out OUT, int TR, int NC>
 __global__ __launch_bounds__(norm_threads(TR)) void norm_kernel(NormArgs a) {
   __shared__ float lds[2][TR > 64 ? TR / 64 : 1];
@@ -238,7 +238,10 @@ hipError_t norm(const NormArgs &a, int dtype, hipStream_t s) {
 // A group (a wave or a workgroup, as above) walks over rows `groups` apart and
 // keeps the sums for dweight and dbias of its columns in registers, so dy and
 // x are read once; its two rows of sums go to the workspace, and a second
-// launch adds them up column by column, in a fixed order.
+// launch adds them up column by column, in a fixed order.  512 groups are two
+// workgroups on a compute unit; more would write more sums than they gain (8192
+// x 4096 bfloat16 takes 44 us with 512, 49 with 256, 46 with 768; memory bounds
+// it at 32).
 
 template <typename T, int TR, int NC>
 __global__ __launch_bounds__(norm_threads(TR)) void norm_bwd_kernel(NormBwdArgs a) {
