@@ -7,6 +7,7 @@
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/pybind.h>
 #include <ATen/ATen.h>
 
@@ -290,41 +291,57 @@ std::tuple<Tensor, Tensor, Tensor> layer_norm_backward(const Tensor &dy, const T
   return {dx, dweight, dbias};
 }
 
-std::tuple<Tensor, std::vector<Tensor>> clip_grad_norm(const std::vector<Tensor> &grads, double max_norm, double eps,
-                                                       const std::optional<std::vector<Tensor>> &given,
-                                                       const py::object &stream) {
-  if (grads.empty()) bad_value("no gradients");
-  on_device(grads[0]);
-  if (given && given->size() != grads.size())
-    bad_value(std::to_string(grads.size()) + " gradients, " + std::to_string(given->size()) + " outputs");
-  const Stream on(grads[0], stream);
-  std::vector<Tensor> out;
-  std::vector<xpose_clip_tensor> table(grads.size());
-  if (given) out = *given; else out.reserve(grads.size());
-  for (size_t i = 0; i < grads.size(); ++i) {
-    const Tensor &g = grads[i];
-    same_device(grads[0], g);
+const Tensor &tensor_of(PyObject *o, const char *what) {
+  if (!THPVariable_Check(o)) bad_type(std::string(what) + ": expected tensors");
+  return THPVariable_Unpack(o);
+}
+
+// (norm, out): `out` is the caller's own sequence, or a new list.
+py::tuple clip_grad_norm(const py::object &given_grads, double max_norm, double eps, const py::object &given_out,
+                         const py::object &stream) {
+  const py::object grads = py::reinterpret_steal<py::object>(PySequence_Fast(given_grads.ptr(), "grads: expected tensors"));
+  if (!grads) throw py::error_already_set();
+  const Py_ssize_t n = PySequence_Fast_GET_SIZE(grads.ptr());
+  if (n == 0) bad_value("no gradients");
+  const bool make = given_out.is_none();
+  py::object out;
+  if (make) {
+    out = py::list(n);
+  } else {
+    out = py::reinterpret_steal<py::object>(PySequence_Fast(given_out.ptr(), "out: expected tensors"));
+    if (!out) throw py::error_already_set();
+    if (PySequence_Fast_GET_SIZE(out.ptr()) != n)
+      bad_value(std::to_string(n) + " gradients, " + std::to_string(PySequence_Fast_GET_SIZE(out.ptr())) + " outputs");
+  }
+  const Tensor &first = tensor_of(PySequence_Fast_GET_ITEM(grads.ptr(), 0), "grads");
+  on_device(first);
+  const Stream on(first, stream);
+  std::vector<xpose_clip_tensor> table((size_t)n);
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    const Tensor &g = tensor_of(PySequence_Fast_GET_ITEM(grads.ptr(), i), "grads");
+    same_device(first, g);
     const int code = dtype_code(g.scalar_type(), "grads");
     if (!g.is_non_overlapping_and_dense()) bad_value("a gradient does not fill one stretch of memory");
-    if (!given) out.push_back(at::empty_like(g));
-    const Tensor &o = out[i];
-    if (!o.is_same(g)) {
-      same_device(grads[0], o);
+    if (make) PyList_SET_ITEM(out.ptr(), i, THPVariable_Wrap(at::empty_like(g)));
+    const Tensor &o = tensor_of(PySequence_Fast_GET_ITEM(out.ptr(), i), "out");
+    if (!make && !o.is_same(g)) {
+      same_device(first, o);
       if (o.scalar_type() != g.scalar_type() || o.sizes() != g.sizes())
         bad_value("an output differs from its gradient in dtype or shape");
       if (g.numel() && o.strides() != g.strides()) bad_value("an output differs from its gradient in strides");
     }
-    table[i] = {g.data_ptr(), o.data_ptr(), g.numel(), code, 0};
+    table[(size_t)i] = {g.data_ptr(), o.data_ptr(), g.numel(), code, 0};
+    on.record(g, o);
   }
   int64_t size = 0;
-  check(xpose_clip_grad_norm_workspace((int64_t)table.size(), table.data(), &size), "xpose_clip_grad_norm_workspace");
-  Tensor norm = empty({}, at::kFloat, grads[0]), ws = empty({size / 8}, at::kDouble, grads[0]);
-  check(xpose_clip_grad_norm((int64_t)table.size(), table.data(), max_norm, eps, norm.data_ptr<float>(), ws.data_ptr(),
-                             size, on.raw()),
+  check(xpose_clip_grad_norm_workspace(n, table.data(), &size), "xpose_clip_grad_norm_workspace");
+  Tensor norm = empty({}, at::kFloat, first), ws;
+  if (size) ws = empty({size / 8}, at::kDouble, first);
+  check(xpose_clip_grad_norm(n, table.data(), max_norm, eps, norm.data_ptr<float>(),
+                             size ? ws.data_ptr() : nullptr, size, on.raw()),
         "xpose_clip_grad_norm");
   on.record(norm, ws);
-  for (size_t i = 0; i < grads.size(); ++i) on.record(grads[i], out[i]);
-  return {norm, out};
+  return py::make_tuple(norm, make ? out : given_out);
 }
 
 bool is_dense(const Tensor &t) { return t.is_non_overlapping_and_dense(); }

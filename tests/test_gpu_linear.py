@@ -456,7 +456,7 @@ def _grads(shapes, seed, size=1e-2):
             for i, s in enumerate(shapes)]
 
 
-@pytest.mark.parametrize("shapes", [[(1,)], [(7,), (0,), (3, 5)], [(16384,), (16385,)], [(1000, 333), (5,), (2049, 77)],
+@pytest.mark.parametrize("shapes", [[(1,)], [(7,), (0,), (3, 5)], [(16384,), (16385,)], [(1000, 333), (5,), (2049, 77)], [(3,), (4,), (7,), (8,), (9,)],
                                     [(i % 9 + 1, 3) for i in range(250)]])
 @pytest.mark.parametrize("max_norm", [1e9, 0.01, 0.0])
 def test_clip(shapes, max_norm):
