@@ -193,9 +193,12 @@ __device__ inline void reads_and_barrier() {
 // workgroups on a compute unit) spend as many cycles on widening and scaling as
 // on products: 4096^3 takes 130 us (1.06 PFLOP/s).
 //
-// b's rows of one operand: lane l has row 16 (l / 4) + 4 j + l % 4 of the
-// wave's 64, so that over j a lane's results are 16 neighbours in c.  Its place
-// in LDS is 16 j + l.
+// b's rows of one operand: lane l has row 32 (j / 2) + 8 (l / 4) + 4 (j % 2) +
+// l % 4 of the wave's 64, so that over two j a lane's results are 8 neighbours
+// in c, and four lanes' 32: a store writes whole 64-byte pieces of 16 rows
+// (with 16 neighbours a lane, half a 32-byte sector a store, 4096 x 4096 x 1024
+// took 24.0 instead of 23.3 us).  Its place in LDS
+// is 16 j + l.
 template <int TM, int TN, int WM>
 struct Tile {
   static constexpr int WN = 64;
@@ -263,8 +266,7 @@ __global__ __launch_bounds__((Tile<TM, TN, WM>::THREADS), 2) void fp8_tile_kerne
   const int64_t bytes_a = (p.m - m0 - 1) * p.lda + p.k, bytes_b = (p.n - n0 - 1) * p.ldb + p.k;
   const int row_in = wave * 8 + lane / 8;  // of kRows
   const int at = ((lane % 8) ^ swizzle(row_in)) * 16;
-  const int row_in_b = row_in % 16 / 4 * 16 + row_in / 16 * 4 + row_in % 4;
-  auto first_b = [](int i) { return kRows == 64 ? i * 64 : i / 2 * 64 + i % 2 * 8; };
+  const int row_in_b = row_in / 32 * 32 + row_in % 16 / 4 * 8 + row_in / 16 % 2 * 4 + row_in % 4;
   const uint32_t off_a = (uint32_t)row_in * (uint32_t)p.lda + at;
   const uint32_t off_b = (uint32_t)row_in_b * (uint32_t)p.ldb + at;
   const int rows_a = (int)(p.m - m0 < TM ? p.m - m0 : TM) - 1;
@@ -286,7 +288,7 @@ __global__ __launch_bounds__((Tile<TM, TN, WM>::THREADS), 2) void fp8_tile_kerne
 #pragma unroll
   for (int i = 0; i < LA; ++i) from_a[i] = buffer(a0 + i * kRows * p.lda, bytes_a - i * kRows * p.lda);
 #pragma unroll
-  for (int i = 0; i < LB; ++i) from_b[i] = buffer(b0 + first_b(i) * p.ldb, bytes_b - first_b(i) * p.ldb);
+  for (int i = 0; i < LB; ++i) from_b[i] = buffer(b0 + i * kRows * p.ldb, bytes_b - i * kRows * p.ldb);
   auto stage_a = [&](int kb, uint8_t *buf) {
 #pragma unroll
     for (int i = 0; i < LA; ++i)
@@ -310,7 +312,7 @@ __global__ __launch_bounds__((Tile<TM, TN, WM>::THREADS), 2) void fp8_tile_kerne
     }
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
-      const uint8_t *row = b + min(first_b(i) + row_in_b, rows_b) * p.ldb;
+      const uint8_t *row = b + min(i * kRows + row_in_b, rows_b) * p.ldb;
       from_b[i] = load_chunk(row + at, tail - at, row);
     }
 #pragma unroll
@@ -341,8 +343,8 @@ __global__ __launch_bounds__((Tile<TM, TN, WM>::THREADS), 2) void fp8_tile_kerne
   const int x = swizzle(l16), lo = (g ^ x) * 16, hi = ((g + 4) ^ x) * 16;
   const int place_a = T::A + (wm + l16) * kBlock, place_b = T::B + (wn + l16) * kBlock;
   const int place_sa = T::SA + 4 * (wm + l16);
-  const int place_sb = T::SB + 4 * (MODE == kFp8Pow2   ? wn + l16 / 4 * 16 + l16 % 4
-                                    : MODE == kFp8Rows ? wn + 16 * g
+  const int place_sb = T::SB + 4 * (MODE == kFp8Pow2   ? wn + l16 / 4 * 8 + l16 % 4
+                                    : MODE == kFp8Rows ? wn + 8 * g
                                                        : wn);  // 64 rows of one tile
   auto read_a = [&](const uint8_t *buf, int i) {
     Rows16 v;
@@ -355,9 +357,9 @@ __global__ __launch_bounds__((Tile<TM, TN, WM>::THREADS), 2) void fp8_tile_kerne
     Rows16 v;
     v.lo = *reinterpret_cast<const u32x4 *>(buf + (place_b + lo) + j * 16 * kBlock);
     v.hi = *reinterpret_cast<const u32x4 *>(buf + (place_b + hi) + j * 16 * kBlock);
-    if constexpr (MODE == kFp8Pow2) v.scale = *reinterpret_cast<const float *>(buf + place_sb + j * 16);
+    if constexpr (MODE == kFp8Pow2) v.scale = *reinterpret_cast<const float *>(buf + place_sb + j / 2 * 128 + j % 2 * 16);
     if constexpr (MODE == kFp8Tiles) v.scale = *reinterpret_cast<const float *>(buf + place_sb);
-    if constexpr (MODE == kFp8Rows) v.scales = *reinterpret_cast<const f32x4 *>(buf + place_sb + j * 16);
+    if constexpr (MODE == kFp8Rows) v.scales = *reinterpret_cast<const f32x4 *>(buf + place_sb + j / 2 * 128 + j % 2 * 16);
     return v;
   };
 
@@ -442,15 +444,18 @@ __global__ __launch_bounds__((Tile<TM, TN, WM>::THREADS), 2) void fp8_tile_kerne
   if (s < steps) block(s, bool_constant<false>{}, bool_constant<false>{});
 
   uint8_t *c = (uint8_t *)p.c + (int64_t)split * p.slice * 4;  // slices are float32
-  const int64_t col = n0 + wn + 16 * g;
 #pragma unroll
   for (int i = 0; i < T::NI; ++i) {
     const int64_t row = m0 + wm + 16 * i + l16;
-    if (row >= p.m || col >= p.n) continue;
-    float f[16];
+    if (row >= p.m) continue;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) f[e] = acc[i][e / 4][e % 4];
-    store_run<16>(c, p.out, row * p.ldc + col, p.n - col, f);
+    for (int h = 0; h < 2; ++h) {
+      const int64_t col = n0 + wn + 32 * h + 8 * g;
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = acc[i][2 * h + e / 4][e % 4];
+      if (col < p.n) store_run<8>(c, p.out, row * p.ldc + col, p.n - col, f);
+    }
   }
 }
 
