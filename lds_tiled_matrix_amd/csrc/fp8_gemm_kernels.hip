@@ -479,7 +479,8 @@ hipError_t launch_tile(const Fp8GemmArgs &a, Fp8GemmMode mode, hipStream_t s) {
 // of a; its waves take the blocks of k in turn, straight from memory into the
 // instruction's registers, two or four at a time, and their sums are added through
 // LDS in the waves' order.  One token through 4096 x 4096 takes 5.9 us (2.8 TB/s;
-// the launch is over half of it), through 4096 x 8192 8 us.
+// the launch is over half of it), through 4096 x 8192 8 us.  A long k and few
+// rows of b go in slices, as for the tiles.
 constexpr int kSkinnyWaves = 8;
 
 template <int MS, bool EXACT>
@@ -488,9 +489,12 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void fp8_skinny_kernel(Fp8GemmAr
   __shared__ __align__(16) float sums[kSkinnyWaves][MS][64][4];
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
   const int l16 = lane % 16, g = lane / 16;
-  const int64_t n0 = (int64_t)(blockIdx.x % p.tiles_n) * 16;
-  const int64_t m0 = (int64_t)(blockIdx.x / p.tiles_n) * 16 * MS;
-  const int64_t blocks = (p.k + kBlock - 1) / kBlock;
+  const uint32_t tiles = p.tiles_m * p.tiles_n, split = blockIdx.x / tiles, id = blockIdx.x % tiles;
+  const int64_t n0 = (int64_t)(id % p.tiles_n) * 16;
+  const int64_t m0 = (int64_t)(id / p.tiles_n) * 16 * MS;
+  // this slice's blocks of k, from `first` to before `blocks`
+  const int64_t first = (int64_t)split * p.blocks_per_split;
+  const int64_t blocks = min((p.k + kBlock - 1) / kBlock, first + p.blocks_per_split);
 
   const int64_t brow = n0 + l16 < p.n ? n0 + l16 : p.n - 1;
   const uint8_t *b = p.b + brow * p.ldb;
@@ -512,7 +516,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void fp8_skinny_kernel(Fp8GemmAr
   f32x4 acc[MS];
 #pragma unroll
   for (int i = 0; i < MS; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int64_t kb0 = wave; kb0 < blocks; kb0 += kSkinnyWaves * kDepth) {
+  for (int64_t kb0 = first + wave; kb0 < blocks; kb0 += kSkinnyWaves * kDepth) {
     u32x4 bv[kDepth][2], av[kDepth][MS][2];
     float sav[kDepth][MS], sbv[kDepth][4];
 #pragma unroll
@@ -561,7 +565,8 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void fp8_skinny_kernel(Fp8GemmAr
     const int64_t row = m0 + 16 * i + l16, col = n0 + 4 * g;
     if (row < p.m && col < p.n) {
       const float f[4] = {s[0], s[1], s[2], s[3]};
-      store_run<4>(p.c, p.out, row * p.ldc + col, p.n - col, f);
+      uint8_t *c = (uint8_t *)p.c + (int64_t)split * p.slice * 4;  // slices are float32
+      store_run<4>(c, p.out, row * p.ldc + col, p.n - col, f);
     }
   }
 }
@@ -571,7 +576,7 @@ hipError_t launch_skinny(const Fp8GemmArgs &a, Fp8GemmMode, hipStream_t s) {
   Fp8GemmArgs copy = a;
   void *args[] = {&copy};
   return hipLaunchKernel(reinterpret_cast<const void *>(&fp8_skinny_kernel<MS, EXACT>),
-                         dim3(a.tiles_m * a.tiles_n), dim3(64 * kSkinnyWaves), args, 0, s);
+                         dim3(a.tiles_m * a.tiles_n * a.splits), dim3(64 * kSkinnyWaves), args, 0, s);
 }
 
 template <int TM, int TN, int WM, bool EXACT>

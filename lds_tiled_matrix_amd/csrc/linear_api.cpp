@@ -99,14 +99,13 @@ constexpr int64_t kMaxSplits = 16;
 // Estimated microseconds of a product on MI355X, for choosing among kernels.
 // Fitted to 160 shapes from 1 x 64 x 128 to 5000 x 4096 x 8192, with bfloat16
 // and with float32 results, each timed with every kernel and 1 to 16 slices:
-// the choice is within 10% of the fastest for all but two of them, 15% at
-// worst.
+// the choice is within 12% of the fastest for all but one of them, which takes
+// 17% more.
 //
 // Tiles: a start, then a block of k takes `one` while the compute units hold a
 // workgroup each and `two` with two of the 128 x 128 tiles on each (of 256 x
 // 256 only one fits); a lone workgroup waits for memory, so that the second
-// costs about half as much again.  Slices are written and read as float32 by a
-// launch of its own.
+// costs about half as much again.
 double tile_time(const xpose::Fp8GemmKernel &kern, int64_t tiles, int64_t splits,
                  int64_t blocks, double outputs, int out_size) {
   const bool large = kern.tile_m == 256;
@@ -114,22 +113,18 @@ double tile_time(const xpose::Fp8GemmKernel &kern, int64_t tiles, int64_t splits
   const double two = large ? 3.5 : kern.exact ? 1.75 : 1.15;
   const int64_t groups = tiles * splits, rest = groups % 512;
   const double rounds = (double)(groups / 512) * two + (rest > 256 ? two : rest ? one : 0);
-  double t = (large ? 5.0 : 3.3) + rounds * (double)ceil_div(blocks, splits) +
-             outputs * out_size / 4e6;
-  if (splits > 1) t += 2.2 + outputs * (8.0 * splits + out_size) / 4e6;
-  return t;
+  return (large ? 5.0 : 3.3) + rounds * (double)ceil_div(blocks, splits) + outputs * out_size / 4e6;
 }
 
-// Few rows: rounds of the workgroups that fit at once; a block of k costs more
+// Few rows: rounds of a workgroup a compute unit; a block of k costs more
 // where it is not among the first 16, which are on their way together, and with
 // more rows of a to read for it.
 double skinny_time(const xpose::Fp8GemmKernel &kern, int64_t groups, int64_t blocks) {
   const bool wide = kern.tile_m == 64;
-  const int64_t at_once = wide ? 256 : 512;
   const double first = wide ? 0.17 : kern.tile_m == 32 ? 0.12 : 0.04;
   const double later = wide ? 0.25 : kern.tile_m == 32 ? 0.165 : 0.085;
   const double b = (double)std::min<int64_t>(blocks, 16), more = (double)blocks - b;
-  return 0.8 + (double)ceil_div(groups, at_once) * ((wide ? 2.9 : 2.5) + first * b + later * more);
+  return 0.8 + (double)ceil_div(groups, 256) * ((wide ? 2.9 : 2.5) + first * b + later * more);
 }
 
 int plan_gemm(int64_t m, int64_t n, int64_t k, int out_dtype, GemmPlan &plan) {
@@ -147,7 +142,7 @@ int plan_gemm(int64_t m, int64_t n, int64_t k, int out_dtype, GemmPlan &plan) {
     int64_t tiles;
     if (__builtin_mul_overflow(tiles_m, tiles_n, &tiles) || tiles > kMaxGrid / kMaxSplits)
       continue;
-    const int64_t most = kern.skinny || kern.tile_m == 256 ? 1 : kMaxSplits;
+    const int64_t most = kern.tile_m == 256 ? 1 : kMaxSplits;
     for (int64_t want = 1; want <= most && want <= blocks; ++want) {
       const int64_t per = ceil_div(blocks, want), splits = ceil_div(blocks, per);
       if (splits != want) continue;
@@ -155,8 +150,10 @@ int plan_gemm(int64_t m, int64_t n, int64_t k, int out_dtype, GemmPlan &plan) {
       if (splits > 1 && (__builtin_mul_overflow(m, n, &bytes) ||
                          __builtin_mul_overflow(bytes, 4 * splits, &bytes)))
         continue;
-      const double t = kern.skinny ? skinny_time(kern, tiles, blocks)
-                                   : tile_time(kern, tiles, splits, blocks, outputs, exact ? 4 : 2);
+      double t = kern.skinny ? skinny_time(kern, tiles * splits, per)
+                             : tile_time(kern, tiles, splits, blocks, outputs, exact ? 4 : 2);
+      // slices are written and read as float32, the latter by a launch of its own
+      if (splits > 1) t += 2.2 + outputs * (8.0 * (double)splits + (exact ? 4 : 2)) / 4e6;
       if (!plan.kernel || t < best) {
         best = t;
         plan = GemmPlan{&kern, tiles_m, tiles_n, per, splits, bytes};

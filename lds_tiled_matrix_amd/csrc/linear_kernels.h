@@ -27,7 +27,7 @@ enum Fp8GemmMode { kFp8Rows, kFp8Tiles, kFp8Pow2 };  // what scale_b looks like
 
 struct Fp8GemmKernel {
   int tile_m, tile_n, threads;
-  bool skinny;  // waves share out k among themselves: no other split
+  bool skinny;  // waves share out k among themselves
   bool exact;   // for float32 results: products summed in full
   hipError_t (*launch)(const Fp8GemmArgs &, Fp8GemmMode, hipStream_t);
 };

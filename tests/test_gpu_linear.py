@@ -104,6 +104,14 @@ def test_gemm(m, n, k, block_rows, pow2):
         _close(got, want, tol, dtype)
 
 
+@pytest.mark.parametrize("m,n,k", [(3, 200, 8200), (24, 90, 7360), (60, 33, 9001)])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_gemm_few_rows_in_slices(m, n, k, block_rows):
+    info = X.fp8_gemm_plan(m, n, k, block_rows=block_rows)
+    assert info["tile_n"] == 16 and info["splits"] > 1
+    test_gemm(m, n, k, block_rows, False)
+
+
 @pytest.mark.parametrize("m,n,k,block_rows,pow2", [
     (4000, 4090, 400, 128, False), (3850, 4096, 400, 1, False), (4096, 3999, 400, 128, True),
     (3901, 4090, 390, 1, True), (4000, 4090, 512, 1, False)])
