@@ -238,10 +238,9 @@ hipError_t norm(const NormArgs &a, int dtype, hipStream_t s) {
 // A group (a wave or a workgroup, as above) walks over rows `groups` apart and
 // keeps the sums for dweight and dbias of its columns in registers, so dy and
 // x are read once; its two rows of sums go to the workspace, and a second
-// launch adds them up column by column, in a fixed order.  512 groups are two
-// workgroups on a compute unit; more would write more sums than they gain (8192
-// x 4096 bfloat16 takes 44 us with 512, 49 with 256, 46 with 768; memory bounds
-// it at 32).
+// launch adds them up column by column, in a fixed order.  8192 x 4096
+// bfloat16 takes 44 us (4.6 TB/s; memory bounds it at 32).  Two rows' loads under
+// way instead of one gain nothing.
 
 template <typename T, int TR, int NC>
 __global__ __launch_bounds__(norm_threads(TR)) void norm_bwd_kernel(NormBwdArgs a) {
@@ -456,11 +455,20 @@ hipError_t launch_layer_norm_quantize(const NormArgs &a, int dtype, bool pow2, h
   return pow2 ? norm<kE4m3Pow2>(a, dtype, s) : norm<kE4m3>(a, dtype, s);
 }
 
-// Enough groups that every compute unit has loads under way, few enough that
-// their sums are little next to dy and x.
+// A group's rows cost time one after the other; every group writes two rows of
+// sums, which are read again.  The least of both lies near sqrt(32 rows) groups
+// (sqrt(48 rows) where a group is a wave), and powers of two load the 256
+// compute units evenly (3001 x 2999: 29 us with 512 groups, 37 with 334).  There
+// is no gain from more than what runs at once: two workgroups on a compute unit,
+// one for rows over 4096 columns.  Against as many groups as rows, at most 512
+// (2048 to 1024 columns), bfloat16: 512 x 4096 18.0 -> 12.4 us, 2048 x 8192 34.4
+// -> 26.9, 4096 x 1024 23.5 -> 16.6.
 int norm_bwd_groups(int64_t rows, int64_t cols) {
-  const int64_t most = cols <= 1024 ? 2048 : 512;
-  return (int)(rows < most ? rows : most);
+  const int64_t most = cols <= 1024 ? 2048 : cols <= 4096 ? 512 : 256;
+  const int64_t weight = cols <= 1024 ? 48 : 32;
+  int64_t groups = 1;
+  while (groups < most && groups * groups < weight * rows) groups *= 2;
+  return (int)(rows < groups ? rows : groups);
 }
 int64_t norm_bwd_row_floats(int64_t rows, int64_t cols) {
   return cols > kLongBwd ? 2 * rows : 0;
