@@ -374,11 +374,11 @@ int xpose_layer_norm_quantize(int64_t rows, int64_t cols, const void *x,
 }
 
 // Floats of workspace: the rows' sums where the kernel needs them, then two
-// partial gradients a group.
+// partial gradients a workgroup.
 static int bwd_floats(int64_t rows, int64_t cols, int64_t *floats) {
-  const int64_t groups = xpose::norm_bwd_groups(rows, cols);
+  const int64_t parts = xpose::norm_bwd_parts(rows, cols);
   int64_t f;
-  if (__builtin_mul_overflow(2 * groups, cols, &f) ||
+  if (__builtin_mul_overflow(2 * parts, cols, &f) ||
       __builtin_add_overflow(f, xpose::norm_bwd_row_floats(rows, cols), &f) ||
       f > INT64_MAX / 4)
     return XPOSE_EINVAL;
@@ -409,7 +409,7 @@ int xpose_layer_norm_backward(int64_t rows, int64_t cols, const void *dy,
   if (rc != XPOSE_OK) return rc;
   // the long-row kernels' grid
   if (ceil_div(cols, 64) > kMaxGrid / 2 ||
-      (cols > 0 && xpose::norm_bwd_groups(rows, cols) > kMaxGrid / ceil_div(cols, 2048)))
+      (cols > 0 && xpose::norm_bwd_parts(rows, cols) > kMaxGrid / ceil_div(cols, 2048)))
     return XPOSE_EINVAL;
   Ranges r;
   r.matrix(dy, rows, cols, lddy, size, size, false);
@@ -444,7 +444,7 @@ int xpose_layer_norm_backward(int64_t rows, int64_t cols, const void *dy,
   a.ldx = ldx;
   a.lddx = lddx;
   a.param_dtype = param_dtype;
-  a.groups = xpose::norm_bwd_groups(rows, cols);
+  a.parts = xpose::norm_bwd_parts(rows, cols);
   return hip(xpose::launch_layer_norm_backward(a, dtype, (hipStream_t)stream));
 }
 

@@ -127,12 +127,15 @@ __device__ inline uint32_t max16(uint32_t x) {
   return max(x, rotate16<1>(x));
 }
 
-// The sum over a wave's 64 lanes, in every lane.
-__device__ inline float sum64(float x) {
+// The sum over this lane's row of 16, and over a wave's 64 lanes, in every lane.
+__device__ inline float sum16(float x) {
   x += __uint_as_float(rotate16<8>(__float_as_uint(x)));
   x += __uint_as_float(rotate16<4>(__float_as_uint(x)));
   x += __uint_as_float(rotate16<2>(__float_as_uint(x)));
-  x += __uint_as_float(rotate16<1>(__float_as_uint(x)));
+  return x + __uint_as_float(rotate16<1>(__float_as_uint(x)));
+}
+__device__ inline float sum64(float x) {
+  x = sum16(x);
   x += __shfl_xor(x, 16);
   return x + __shfl_xor(x, 32);
 }

@@ -96,11 +96,11 @@ struct NormBwdArgs {
   float *dweight, *dbias, *partial;
   int64_t rows, cols, lddy, ldx, lddx;
   int32_t param_dtype;
-  int32_t groups;  // partial sums of each gradient
+  int32_t parts;  // partial sums of each gradient
 };
 // How many partial sums of `cols` values the backward pass of these sizes
 // takes, and how many floats of row sums before them.
-int norm_bwd_groups(int64_t rows, int64_t cols);
+int norm_bwd_parts(int64_t rows, int64_t cols);
 int64_t norm_bwd_row_floats(int64_t rows, int64_t cols);
 hipError_t launch_layer_norm_backward(const NormBwdArgs &, int dtype,
                                       hipStream_t);

@@ -15,7 +15,9 @@ namespace {
 // eight neighbouring columns a lane: it is read once, and the variance is the
 // mean of the centred squares, not a difference of large sums.
 //
-// TR is 64 (a wave a row, four rows a workgroup) or the whole workgroup.
+// TR is 16 (a row of up to 256 columns to a quarter of a wave), 64 (a wave a
+// row) or the whole workgroup.  Short rows on 64 lanes leave most of them idle:
+// 100000 x 128 bfloat16 took 32 us.
 
 // Weights and biases: float32, or of the input's 16-bit types.
 __device__ inline void load_param8(const void *p, int dtype, int64_t col, int valid, float none, float (&f)[8]) {
@@ -36,12 +38,13 @@ __device__ inline int in_row(int64_t cols, int64_t col) {
   return left < 0 ? 0 : left > 8 ? 8 : (int)left;
 }
 
-// Sums over the lanes of a row, the same in all of them.  With one wave a row
-// no LDS is needed; else `lds` holds a float for each wave, and two calls in
+// Sums over the lanes of a row, the same in all of them.  Within a wave no LDS
+// is needed; else `lds` holds a float for each wave, and two calls in
 // turn use two of them, so that one barrier a call is enough: who writes to the
 // first one again has passed the second's barrier, behind everybody's reads.
 template <int TR>
 __device__ inline float row_sum(float x, float *lds) {
+  if constexpr (TR == 16) return sum16(x);
   x = sum64(x);
   if constexpr (TR > 64) {
     if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = x;
@@ -64,7 +67,12 @@ __device__ inline void put_chunk(const NormArgs &a, int64_t row, int64_t col, in
     // the 16 lanes of a DPP row hold the 128 columns of one block
     uint32_t m = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, e < valid ? magnitude(y[e]) : 0u);
+    for (int e = 0; e < 8; ++e) m = max(m, magnitude(y[e]));
+    if (valid < 8) {
+      m = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max(m, e < valid ? magnitude(y[e]) : 0u);
+    }
     m = max16(m);
     const float scale = scale_of<OUT == kE4m3Pow2>(m);
     if (threadIdx.x % 16 == 0 && valid > 0) a.scale[(col >> 7) * a.ld_scale + row] = scale;
@@ -84,7 +92,7 @@ __device__ inline void put_chunk(const NormArgs &a, int64_t row, int64_t col, in
   }
 }
 
-constexpr int norm_threads(int tr) { return tr == 64 ? 256 : tr; }
+constexpr int norm_threads(int tr) { return tr <= 64 ? 256 : tr; }
 
 // Workgroups stay: a group of TR lanes walks over rows `groups` apart with the
 // weight and bias in registers (read anew for each row they are four times a
@@ -96,7 +104,7 @@ __global__ __launch_bounds__(norm_threads(TR)) void norm_kernel(NormArgs a) {
   const int lane = threadIdx.x % TR;
   const int64_t first = (int64_t)blockIdx.x * (norm_threads(TR) / TR) + threadIdx.x / TR;
   const int64_t groups = (int64_t)gridDim.x * (norm_threads(TR) / TR);
-  if (first >= a.rows) return;  // whole waves, and none where barriers follow
+  if (first >= a.rows) return;  // whole groups, and none where barriers follow
   float w[NC][8], b[NC][8];
   Vec8<T> ahead[NC];
   auto fetch = [&](int64_t row) {
@@ -130,10 +138,14 @@ __global__ __launch_bounds__(norm_threads(TR)) void norm_kernel(NormArgs a) {
     for (int i = 0; i < NC; ++i) {
       const int valid = in_row(a.cols, (i * TR + lane) * 8);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[i][e] = e < valid ? v[i][e] - mean : 0.f;
-        s = __builtin_fmaf(v[i][e], v[i][e], s);
+      for (int e = 0; e < 8; ++e) v[i][e] -= mean;
+      if (valid < 8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e >= valid) v[i][e] = 0.f;
       }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s = __builtin_fmaf(v[i][e], v[i][e], s);
     }
     const float rstd = 1.f / sqrtf(row_sum<TR>(s, lds[1]) / (float)a.cols + a.eps);
     if (lane == 0 && a.mean) {
@@ -217,6 +229,8 @@ hipError_t launch_norm(const NormArgs &a, hipStream_t s) {
 }
 template <typename T, Out OUT>
 hipError_t norm(const NormArgs &a, hipStream_t s) {
+  if (a.cols <= 128) return launch_norm<T, OUT, 16, 1>(a, s);
+  if (a.cols <= 256) return launch_norm<T, OUT, 16, 2>(a, s);
   if (a.cols <= 512) return launch_norm<T, OUT, 64, 1>(a, s);
   if (a.cols <= 1024) return launch_norm<T, OUT, 64, 2>(a, s);
   if (a.cols <= 2048) return launch_norm<T, OUT, 256, 1>(a, s);
@@ -235,19 +249,22 @@ hipError_t norm(const NormArgs &a, int dtype, hipStream_t s) {
 
 // ----- the backward pass -----------------------------------------------------
 //
-// A group (a wave or a workgroup, as above) walks over rows `groups` apart and
-// keeps the sums for dweight and dbias of its columns in registers, so dy and
-// x are read once; its two rows of sums go to the workspace, and a second
-// launch adds them up column by column, in a fixed order.  8192 x 4096
-// bfloat16 takes 44 us (4.6 TB/s; memory bounds it at 32).  Two rows' loads under
-// way instead of one gain nothing.
+// A group of TR lanes walks over rows `groups` apart and keeps the sums for
+// dweight and dbias of its columns in registers, so dy and x are read once; the
+// workgroup's two rows of sums go to the workspace, and a second launch adds
+// them up column by column, all in a fixed order.  8192 x 4096 bfloat16 takes
+// 44 us (4.6 TB/s; memory bounds it at 32).  Two rows' loads under way instead of
+// one gain nothing.
+// Short rows: 100000 x 128 bfloat16 takes 22 us, 76 with a wave a row and a sum
+// a wave; 4096 x 1024 11.8 us, 16.6 with a sum a wave.
 
 template <typename T, int TR, int NC>
 __global__ __launch_bounds__(norm_threads(TR)) void norm_bwd_kernel(NormBwdArgs a) {
+  constexpr int kPer = norm_threads(TR) / TR;  // of a workgroup
   __shared__ float lds[2][2][TR > 64 ? TR / 64 : 1];
-  const int lane = threadIdx.x % TR;
-  const int group = blockIdx.x * (norm_threads(TR) / TR) + threadIdx.x / TR;
-  if (group >= a.groups) return;
+  __shared__ __align__(16) float joined[kPer > 1 ? 3 : 1][2][kPer > 1 ? NC * TR * 8 : 4];
+  const int lane = threadIdx.x % TR, wave = threadIdx.x / 64;
+  const int64_t group = (int64_t)blockIdx.x * kPer + threadIdx.x / TR, groups = (int64_t)a.parts * kPer;
   float w[NC][8], dw[NC][8], db[NC][8];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
@@ -270,9 +287,9 @@ __global__ __launch_bounds__(norm_threads(TR)) void norm_bwd_kernel(NormBwdArgs 
       next_x[i] = load_raw8((const T *)a.x + row * a.ldx + col, valid);
     }
   };
-  fetch(group);
+  if (group < a.rows) fetch(group);
   int turn = 0;
-  for (int64_t row = group; row < a.rows; row += a.groups, turn ^= 1) {
+  for (int64_t row = group; row < a.rows; row += groups, turn ^= 1) {
     const float mean = next_mean, rstd = next_rstd;
     float dy[NC][8], x[NC][8];
     float s1 = 0.f, s2 = 0.f;
@@ -283,7 +300,7 @@ __global__ __launch_bounds__(norm_threads(TR)) void norm_bwd_kernel(NormBwdArgs 
         dy[i][e] = at8<T>(next_dy[i], e);
         x[i][e] = at8<T>(next_x[i], e);
       }
-    if (row + a.groups < a.rows) fetch(row + a.groups);
+    if (row + groups < a.rows) fetch(row + groups);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
 #pragma unroll
@@ -297,8 +314,8 @@ __global__ __launch_bounds__(norm_threads(TR)) void norm_bwd_kernel(NormBwdArgs 
       }
     }
     // both sums behind one barrier; the next row uses the other half of lds
-    s1 = sum64(s1);
-    s2 = sum64(s2);
+    s1 = TR == 16 ? sum16(s1) : sum64(s1);
+    s2 = TR == 16 ? sum16(s2) : sum64(s2);
     if constexpr (TR > 64) {
       if (threadIdx.x % 64 == 0) {
         lds[turn][0][threadIdx.x / 64] = s1;
@@ -325,7 +342,38 @@ __global__ __launch_bounds__(norm_threads(TR)) void norm_bwd_kernel(NormBwdArgs 
       store8((T *)a.dx + row * a.lddx + col, in_row(a.cols, col), d);
     }
   }
-  float *p = a.partial + (int64_t)group * 2 * a.cols;
+  if constexpr (kPer > 1) {  // four waves' sums, first of the groups in each
+    if constexpr (TR == 16) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dw[i][e] += __shfl_xor(dw[i][e], 16);
+          dw[i][e] += __shfl_xor(dw[i][e], 32);
+          db[i][e] += __shfl_xor(db[i][e], 16);
+          db[i][e] += __shfl_xor(db[i][e], 32);
+        }
+    }
+    if (wave > 0 && threadIdx.x % 64 < TR) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        store8(&joined[wave - 1][0][(i * TR + lane) * 8], 8, dw[i]);
+        store8(&joined[wave - 1][1][(i * TR + lane) * 8], 8, db[i]);
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x >= TR) return;
+#pragma unroll
+    for (int v = 0; v < 3; ++v)
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dw[i][e] += joined[v][0][(i * TR + lane) * 8 + e];
+          db[i][e] += joined[v][1][(i * TR + lane) * 8 + e];
+        }
+  }
+  float *p = a.partial + (int64_t)blockIdx.x * 2 * a.cols;
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int64_t col = (i * TR + lane) * 8;
@@ -374,7 +422,7 @@ __global__ __launch_bounds__(256) void norm_bwd_long_kernel(NormBwdArgs a) {
   const int valid = in_row(a.cols, col);
   float w[8], dw[8] = {}, db[8] = {};
   load_param8(a.weight, a.param_dtype, col, valid, 1.f, w);
-  for (int64_t row = group; row < a.rows; row += a.groups) {
+  for (int64_t row = group; row < a.rows; row += a.parts) {
     const float mean = a.mean[row], rstd = a.rstd[row];
     const float s1 = a.partial[2 * row], s2 = a.partial[2 * row + 1];
     float dy[8], x[8], d[8];
@@ -409,7 +457,7 @@ __global__ __launch_bounds__(64 * kParamWaves) void norm_bwd_params_kernel(NormB
   if (col < a.cols) {
     const float *p = a.partial + which * a.cols + col;
 #pragma unroll 8
-    for (int g = wave; g < a.groups; g += kParamWaves) s += p[(int64_t)g * 2 * a.cols];
+    for (int g = wave; g < a.parts; g += kParamWaves) s += p[(int64_t)g * 2 * a.cols];
   }
   lds[wave][lane] = s;
   __syncthreads();
@@ -429,12 +477,13 @@ hipError_t launch(const void *kernel, const NormBwdArgs &a, int64_t grid, int th
 }
 template <typename T, int TR, int NC>
 hipError_t launch_bwd(const NormBwdArgs &a, hipStream_t s) {
-  constexpr int per = norm_threads(TR) / TR;
   return launch(reinterpret_cast<const void *>(&norm_bwd_kernel<T, TR, NC>), a,
-                (a.groups + per - 1) / per, norm_threads(TR), s);
+                a.parts, norm_threads(TR), s);
 }
 template <typename T>
 hipError_t norm_bwd(const NormBwdArgs &a, hipStream_t s) {
+  if (a.cols <= 128) return launch_bwd<T, 16, 1>(a, s);
+  if (a.cols <= 256) return launch_bwd<T, 16, 2>(a, s);
   if (a.cols <= 512) return launch_bwd<T, 64, 1>(a, s);
   if (a.cols <= 1024) return launch_bwd<T, 64, 2>(a, s);
   if (a.cols <= 2048) return launch_bwd<T, 256, 1>(a, s);
@@ -443,7 +492,7 @@ hipError_t norm_bwd(const NormBwdArgs &a, hipStream_t s) {
   hipError_t e = launch(reinterpret_cast<const void *>(&norm_bwd_sums_kernel<T>), a, a.rows, kLongThreads, s);
   if (e != hipSuccess) return e;
   return launch(reinterpret_cast<const void *>(&norm_bwd_long_kernel<T>), a,
-                (a.cols + kLongBlock - 1) / kLongBlock * a.groups, 256, s);
+                (a.cols + kLongBlock - 1) / kLongBlock * a.parts, 256, s);
 }
 
 }  // namespace
@@ -455,20 +504,25 @@ hipError_t launch_layer_norm_quantize(const NormArgs &a, int dtype, bool pow2, h
   return pow2 ? norm<kE4m3Pow2>(a, dtype, s) : norm<kE4m3>(a, dtype, s);
 }
 
-// A group's rows cost time one after the other; every group writes two rows of
-// sums, which are read again.  The least of both lies near sqrt(32 rows) groups
-// (sqrt(48 rows) where a group is a wave), and powers of two load the 256
-// compute units evenly (3001 x 2999: 29 us with 512 groups, 37 with 334).  There
-// is no gain from more than what runs at once: two workgroups on a compute unit,
-// one for rows over 4096 columns.  Against as many groups as rows, at most 512
-// (2048 to 1024 columns), bfloat16: 512 x 4096 18.0 -> 12.4 us, 2048 x 8192 34.4
-// -> 26.9, 4096 x 1024 23.5 -> 16.6.
-int norm_bwd_groups(int64_t rows, int64_t cols) {
-  const int64_t most = cols <= 1024 ? 2048 : cols <= 4096 ? 512 : 256;
-  const int64_t weight = cols <= 1024 ? 48 : 32;
-  int64_t groups = 1;
-  while (groups < most && groups * groups < weight * rows) groups *= 2;
-  return (int)(rows < groups ? rows : groups);
+// Workgroups, each with two rows of sums in the workspace.  Its rows cost time
+// one after the other, its sums are written and read again.
+// - To 1024 columns (`per` rows at a time, joined into one sum): a row each up
+//   to 256 workgroups, twice as many from eight rows each (bfloat16, 256 against
+//   512: 4096 x 1024 11.8 and 13.2 us, 16384 x 512 20.6 and 16.9).
+// - A row a workgroup: the least of both lies near sqrt(32 rows), and powers of
+//   two load the 256 compute units evenly (3001 x 2999: 29 us with 512, 37 with
+//   334).  No more than run at once: two on a compute unit, or one for rows over
+//   4096 columns (2048 x 8192: 34 us with 512, 27 with 256; 512 x 4096: 18 us
+//   with 512, 12.4 with 128).
+int norm_bwd_parts(int64_t rows, int64_t cols) {
+  if (cols <= 1024) {
+    const int64_t per = cols <= 256 ? 16 : 4, parts = (rows + per - 1) / per;
+    return (int)(parts < 256 ? parts : parts < 8 * 256 ? 256 : 512);
+  }
+  const int64_t most = cols <= 4096 ? 512 : 256;
+  int64_t parts = 1;
+  while (parts < most && parts * parts < 32 * rows) parts *= 2;
+  return (int)(rows < parts ? rows : parts);
 }
 int64_t norm_bwd_row_floats(int64_t rows, int64_t cols) {
   return cols > kLongBwd ? 2 * rows : 0;

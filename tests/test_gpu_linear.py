@@ -433,6 +433,35 @@ def test_layer_norm_backward(rows, cols, dtype):
         assert all(torch.equal(i, j) for i, j in zip(got, again))
 
 
+@pytest.mark.parametrize("rows,cols", [(1, 7), (15, 128), (17, 120), (33, 129), (257, 256), (4099, 64), (9001, 201),
+                                       (33000, 128), (5, 257), (1021, 512), (1025, 1024), (8200, 260)])
+def test_layer_norm_of_short_rows(rows, cols):
+    """Several rows a workgroup, joined into one sum of the parameters'
+    gradients: numbers of rows that fill no workgroup, few and many."""
+    x, w, b = _norm_inputs(rows, cols, F32, rows * cols)
+    dy = torch.from_numpy(np.random.default_rng(rows).standard_normal((rows, cols))).float()
+    xd, wd, bd, dyd = (v.double().numpy() for v in (x, w, b, dy))
+    say(f"short rows {rows} {cols}")
+    want, _, rstd = ol.layer_norm(xd, wd, bd, 1e-5)
+    y, m, r = X.layer_norm(x.to(_dev()), w.to(_dev()), b.to(_dev()), stats=True)
+    _close(_np(y), want, _norm_tol(xd, wd, bd, want, rstd, F32), "y")
+    for pow2 in (False, True):
+        q, s = X.layer_norm_quantize(x.to(_dev()), w.to(_dev()), b.to(_dev()), pow2=pow2)
+        wq, ws = ol.quantize(y.cpu().numpy(), 1, pow2)
+        assert np.array_equal(s.cpu().numpy(), ws) and np.array_equal(_bytes(q), wq)
+    mean, rs = _np(m), _np(r)
+    want = ol.layer_norm_backward(dyd, xd, mean, rs, wd)
+    got = X.layer_norm_backward(dy.to(_dev()), x.to(_dev()), m, r, w.to(_dev()))
+    xhat = np.abs(xd - mean[:, None]) * rs[:, None]
+    g, d = np.abs(dyd * wd), _terms(cols) * U32
+    s1, s2 = g.mean(1, keepdims=True), (g * xhat).mean(1, keepdims=True)
+    dx_tol = (7 * U32 * (g + s1 + xhat * s2) + (d + 3 * U32) * (s1 + 2 * xhat * s2)) * rs[:, None] * 1.01
+    _close(_np(got[0]), want[0], dx_tol, "dx")
+    sums = (rows + 6) * U32
+    _close(_np(got[1]), want[1], sums * np.abs(dyd * xhat).sum(0), "dweight")
+    _close(_np(got[2]), want[2], sums * np.abs(dyd).sum(0), "dbias")
+
+
 def test_layer_norm_backward_is_the_differences_of_the_forward():
     """Central differences of the oracle's forward pass in float64, so that
     only the kernel's own float32 rounding remains: 1e-5 of values near 1
