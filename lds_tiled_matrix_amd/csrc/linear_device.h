@@ -44,6 +44,37 @@ template <typename T>
 __device__ inline float at8(const Vec8<T> &r, int e) {
   if constexpr (sizeof(T) == 4) return r.v[e / 4][e % 4]; else return (float)r.v[e];
 }
+
+// The same of a row of `cols` >= 8 elements, from `col` on, for loads that are to
+// stay under way: element by element they would be waited for at once, to be
+// put together.  Lanes at the row's end load its last eight elements, and
+// `settle8` then moves them to their places.
+template <typename T>
+__device__ inline Vec8<T> load_row8(const T *row, int64_t cols, int64_t col) {
+  return *reinterpret_cast<const Vec8<T> *>(row + (col < cols - 8 ? col : cols - 8));
+}
+template <typename T>
+__device__ inline void settle8(Vec8<T> &v, int64_t cols, int64_t col) {
+  if (col <= cols - 8) return;
+  constexpr int N = 2 * sizeof(T);
+  const int64_t past = col + 8 - cols;
+  const int by = past < 8 ? (int)past : 8;  // elements
+  uint32_t w[N + 1];
+  __builtin_memcpy(w, &v, 4 * N);
+  w[N] = 0;
+  const int words = by * (int)sizeof(T) / 4;
+#pragma unroll
+  for (int d = N; d; d /= 2)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (words & d) w[i] = i + d < N ? w[i + d] : 0;
+  if constexpr (sizeof(T) == 2)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (by & 1) w[i] = w[i] >> 16 | w[i + 1] << 16;
+  __builtin_memcpy(&v, w, 4 * N);
+}
+
 template <typename T>
 __device__ inline void load8(const T *p, int valid, float (&f)[8]) {
   const Vec8<T> r = load_raw8(p, valid);
@@ -202,6 +233,19 @@ struct Quotient {
     const float q = x * r;
     // the remainder's negative, so that a zero keeps its sign
     return __builtin_fmaf(-__builtin_fmaf(q, s, -x), r, q);
+  }
+  // Eight at a time, so that `tiny` is a branch and not two more instructions
+  // for each of them.
+  __device__ void operator()(const float (&x)[8], float (&f)[8]) const {
+    Quotient usual = *this;
+    usual.tiny = false;
+    if (!POW2 && tiny) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = usual(x[e] * up);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = usual(x[e]);
+    }
   }
 };
 

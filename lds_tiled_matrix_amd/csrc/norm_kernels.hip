@@ -78,8 +78,7 @@ __device__ inline void put_chunk(const NormArgs &a, int64_t row, int64_t col, in
     if (threadIdx.x % 16 == 0 && valid > 0) a.scale[(col >> 7) * a.ld_scale + row] = scale;
     const Quotient<OUT == kE4m3Pow2> by(scale, m);
     float f[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = by(y[e]);
+    by(y, f);
     const u32x2 w = {e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7])};
     uint8_t *q = (uint8_t *)a.y + row * a.ldy + col;
     if (valid == 8) {
@@ -97,7 +96,9 @@ constexpr int norm_threads(int tr) { return tr <= 64 ? 256 : tr; }
 // Workgroups stay: a group of TR lanes walks over rows `groups` apart with the
 // weight and bias in registers (read anew for each row they are four times a
 // bfloat16 row's bytes: 8192 x 8192 took 56 us so), and the next row's loads
-// are under way while this one is worked on: 45 us, 6.0 TB/s.
+// are under way while this one is worked on: 45 us, 6.0 TB/s.  Rows of odd
+// lengths: 12345 x 6789 bfloat16 84 us; 107 with loads of single elements at a
+// row's end, which cannot stay under way.
 template <typename T, Out OUT, int TR, int NC>
 __global__ __launch_bounds__(norm_threads(TR)) void norm_kernel(NormArgs a) {
   __shared__ float lds[2][TR > 64 ? TR / 64 : 1];
@@ -111,7 +112,7 @@ __global__ __launch_bounds__(norm_threads(TR)) void norm_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int64_t col = (i * TR + lane) * 8;
-      ahead[i] = load_raw8((const T *)a.x + row * a.ldx + col, in_row(a.cols, col));
+      ahead[i] = load_row8((const T *)a.x + row * a.ldx, a.cols, col);
     }
   };
   fetch(first);
@@ -125,13 +126,16 @@ __global__ __launch_bounds__(norm_threads(TR)) void norm_kernel(NormArgs a) {
     float v[NC][8];
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
+    for (int i = 0; i < NC; ++i) {
+      settle8<T>(ahead[i], a.cols, (i * TR + lane) * 8);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         v[i][e] = at8<T>(ahead[i], e);
         s += v[i][e];
       }
-    if (row + groups < a.rows) fetch(row + groups);
+    }
+    // unconditional: else the new row is copied, and so waited for, at once
+    fetch(row + groups < a.rows ? row + groups : row);
     const float mean = row_sum<TR>(s, lds[0]) / (float)a.cols;
     s = 0.f;
 #pragma unroll
@@ -221,14 +225,25 @@ hipError_t launch(const void *kernel, const NormArgs &a, uint32_t grid, int thre
 }
 template <typename T, Out OUT, int TR, int NC>
 hipError_t launch_norm(const NormArgs &a, hipStream_t s) {
-  // as many workgroups as the registers let run at once, or a few more
-  constexpr int per = norm_threads(TR) / TR, most = 256 * (TR <= 256 ? 6 : TR == 512 ? 3 : 2);
-  const int64_t grid = (a.rows + per - 1) / per;
-  return launch(reinterpret_cast<const void *>(&norm_kernel<T, OUT, TR, NC>), a,
-                (uint32_t)(grid < most ? grid : most), norm_threads(TR), s);
+  constexpr int per = norm_threads(TR) / TR;
+  const void *kernel = reinterpret_cast<const void *>(&norm_kernel<T, OUT, TR, NC>);
+  // as many workgroups as run at once: a few more would run after all others
+  // (16384 x 4096 bfloat16 takes 45 us, 51 with 6 of which 5 fit)
+  static const int at_once = [&] {
+    int n = 0;
+    return hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, norm_threads(TR), 0) == hipSuccess && n > 0 ? n : 1;
+  }();
+  const int64_t grid = (a.rows + per - 1) / per, most = 256 * (int64_t)at_once;
+  return launch(kernel, a, (uint32_t)(grid < most ? grid : most), norm_threads(TR), s);
+}
+template <typename T, Out OUT>
+hipError_t launch_long_norm(const NormArgs &a, hipStream_t s) {
+  return launch(reinterpret_cast<const void *>(&norm_long_kernel<T, OUT>), a,
+                (uint32_t)a.rows, kLongThreads, s);
 }
 template <typename T, Out OUT>
 hipError_t norm(const NormArgs &a, hipStream_t s) {
+  if (a.cols < 8) return launch_long_norm<T, OUT>(a, s);  // shorter than a load
   if (a.cols <= 128) return launch_norm<T, OUT, 16, 1>(a, s);
   if (a.cols <= 256) return launch_norm<T, OUT, 16, 2>(a, s);
   if (a.cols <= 512) return launch_norm<T, OUT, 64, 1>(a, s);
@@ -237,8 +252,7 @@ hipError_t norm(const NormArgs &a, hipStream_t s) {
   if (a.cols <= 4096) return launch_norm<T, OUT, 256, 2>(a, s);
   if (a.cols <= 8192) return launch_norm<T, OUT, 512, 2>(a, s);
   if (a.cols <= 16384) return launch_norm<T, OUT, 1024, 2>(a, s);
-  return launch(reinterpret_cast<const void *>(&norm_long_kernel<T, OUT>), a,
-                (uint32_t)a.rows, kLongThreads, s);
+  return launch_long_norm<T, OUT>(a, s);
 }
 template <Out OUT>
 hipError_t norm(const NormArgs &a, int dtype, hipStream_t s) {
@@ -282,9 +296,8 @@ __global__ __launch_bounds__(norm_threads(TR)) void norm_bwd_kernel(NormBwdArgs 
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int64_t col = (i * TR + lane) * 8;
-      const int valid = in_row(a.cols, col);
-      next_dy[i] = load_raw8((const T *)a.dy + row * a.lddy + col, valid);
-      next_x[i] = load_raw8((const T *)a.x + row * a.ldx + col, valid);
+      next_dy[i] = load_row8((const T *)a.dy + row * a.lddy, a.cols, col);
+      next_x[i] = load_row8((const T *)a.x + row * a.ldx, a.cols, col);
     }
   };
   if (group < a.rows) fetch(group);
@@ -294,13 +307,17 @@ __global__ __launch_bounds__(norm_threads(TR)) void norm_bwd_kernel(NormBwdArgs 
     float dy[NC][8], x[NC][8];
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
+    for (int i = 0; i < NC; ++i) {
+      settle8<T>(next_dy[i], a.cols, (i * TR + lane) * 8);
+      settle8<T>(next_x[i], a.cols, (i * TR + lane) * 8);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         dy[i][e] = at8<T>(next_dy[i], e);
         x[i][e] = at8<T>(next_x[i], e);
       }
-    if (row + groups < a.rows) fetch(row + groups);
+    }
+    // unconditional: else the new row is copied, and so waited for, at once
+    fetch(row + groups < a.rows ? row + groups : row);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
 #pragma unroll
@@ -468,7 +485,8 @@ __global__ __launch_bounds__(64 * kParamWaves) void norm_bwd_params_kernel(NormB
   }
 }
 
-constexpr int64_t kLongBwd = 8192;  // more would spill registers
+// More than 8192 columns would spill registers, under eight are less than a load.
+constexpr bool in_registers(int64_t cols) { return cols >= 8 && cols <= 8192; }
 
 hipError_t launch(const void *kernel, const NormBwdArgs &a, int64_t grid, int threads, hipStream_t s) {
   NormBwdArgs copy = a;
@@ -482,17 +500,19 @@ hipError_t launch_bwd(const NormBwdArgs &a, hipStream_t s) {
 }
 template <typename T>
 hipError_t norm_bwd(const NormBwdArgs &a, hipStream_t s) {
+  if (!in_registers(a.cols)) {
+    hipError_t e = launch(reinterpret_cast<const void *>(&norm_bwd_sums_kernel<T>), a, a.rows, kLongThreads, s);
+    if (e != hipSuccess) return e;
+    return launch(reinterpret_cast<const void *>(&norm_bwd_long_kernel<T>), a,
+                  (a.cols + kLongBlock - 1) / kLongBlock * a.parts, 256, s);
+  }
   if (a.cols <= 128) return launch_bwd<T, 16, 1>(a, s);
   if (a.cols <= 256) return launch_bwd<T, 16, 2>(a, s);
   if (a.cols <= 512) return launch_bwd<T, 64, 1>(a, s);
   if (a.cols <= 1024) return launch_bwd<T, 64, 2>(a, s);
   if (a.cols <= 2048) return launch_bwd<T, 256, 1>(a, s);
   if (a.cols <= 4096) return launch_bwd<T, 256, 2>(a, s);
-  if (a.cols <= kLongBwd) return launch_bwd<T, 512, 2>(a, s);
-  hipError_t e = launch(reinterpret_cast<const void *>(&norm_bwd_sums_kernel<T>), a, a.rows, kLongThreads, s);
-  if (e != hipSuccess) return e;
-  return launch(reinterpret_cast<const void *>(&norm_bwd_long_kernel<T>), a,
-                (a.cols + kLongBlock - 1) / kLongBlock * a.parts, 256, s);
+  return launch_bwd<T, 512, 2>(a, s);
 }
 
 }  // namespace
@@ -525,7 +545,7 @@ int norm_bwd_parts(int64_t rows, int64_t cols) {
   return (int)(rows < parts ? rows : parts);
 }
 int64_t norm_bwd_row_floats(int64_t rows, int64_t cols) {
-  return cols > kLongBwd ? 2 * rows : 0;
+  return in_registers(cols) ? 0 : 2 * rows;
 }
 
 hipError_t launch_layer_norm_backward(const NormBwdArgs &a, int dtype, hipStream_t s) {

@@ -462,6 +462,30 @@ def test_layer_norm_of_short_rows(rows, cols):
     _close(_np(got[2]), want[2], sums * np.abs(dyd).sum(0), "dbias")
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("cols", [*range(1, 25), *range(120, 137), 1021, 2045, 4093, 4099, 8189, 16381])
+def test_norm_reads_no_column_past_the_row(cols, dtype):
+    """Rows inside larger ones that hold NaN: the same bits as rows of their own."""
+    rows = 21
+    x, w, b = _norm_inputs(rows, cols, dtype, cols)
+    dy = torch.from_numpy(np.random.default_rng(cols).standard_normal((rows, cols))).to(dtype).to(_dev())
+    x, w, b = x.to(_dev()), w.to(_dev()), b.to(_dev())
+    def among_nan(t):
+        big = torch.full((rows, cols + 19), math.nan, dtype=dtype, device=_dev())
+        big[:, 9:9 + cols] = t
+        return big[:, 9:9 + cols]
+    say(f"row ends {cols} {dtype}")
+    want = X.layer_norm(x, w, b, stats=True)
+    got = X.layer_norm(among_nan(x), w, b, stats=True)
+    q, s = X.layer_norm_quantize(x, w, b)
+    p, t = X.layer_norm_quantize(among_nan(x), w, b)
+    assert np.array_equal(_bytes(q), _bytes(p)) and torch.equal(s, t)
+    g = X.layer_norm_backward(dy, x, *want[1:], w)
+    h = X.layer_norm_backward(among_nan(dy), among_nan(x), *want[1:], w)
+    for i, j in zip((*want, *g), (*got, *h)):
+        assert torch.equal(i, j) and not i.isnan().any()
+
+
 def test_layer_norm_backward_is_the_differences_of_the_forward():
     """Central differences of the oracle's forward pass in float64, so that
     only the kernel's own float32 rounding remains: 1e-5 of values near 1
