@@ -53,10 +53,23 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(QuantizeArgs a)
   // as they are in memory, and widened at each use: with 16-bit values that
   // is 32 registers instead of 64, and twice the workgroups on a compute unit
   Vec8<T> x[8];
-  const T *src = (const T *)a.x + row * a.ldx + col;
+  const T *src = (const T *)a.x + row * a.ldx;
+  if (r0 + kTile <= a.rows && c0 + kTile <= a.cols) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    x[i] = load_raw8(src + i * a.ldx, i < rows ? cols : 0);
+    for (int i = 0; i < 8; ++i) x[i] = load_raw8(src + i * a.ldx + col, 8);
+  } else if (a.cols >= 8) {  // whole loads here too, all under way together
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] = load_row8((const T *)a.x + (row + i < a.rows ? row + i : a.rows - 1) * a.ldx, a.cols, col);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      settle8<T>(x[i], a.cols, col);
+      if (i >= rows) x[i] = Vec8<T>{};
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = load_raw8(src + i * a.ldx + col, i < rows ? cols : 0);
+  }
 
   uint32_t row_amax[8], tile_amax = 0;
 #pragma unroll

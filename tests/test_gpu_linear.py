@@ -462,6 +462,23 @@ def test_layer_norm_of_short_rows(rows, cols):
     _close(_np(got[2]), want[2], sums * np.abs(dyd).sum(0), "dbias")
 
 
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("rows,cols", [(r, c) for r in (1, 5, 130) for c in (*range(1, 18), *range(121, 140), 261)])
+def test_quantize_reads_nothing_past_the_matrix(rows, cols, dtype, block_rows):
+    x = torch.from_numpy(np.random.default_rng(cols).standard_normal((rows, cols))).to(dtype).to(_dev())
+    big = torch.full((rows + 3, cols + 19), math.nan, dtype=dtype, device=_dev())
+    big[1:rows + 1, 9:9 + cols] = x
+    say(f"matrix ends {rows} {cols} {dtype} {block_rows}")
+    want = X.fp8_quantize(x, block_rows=block_rows, transposed=True)
+    got = X.fp8_quantize(big[1:rows + 1, 9:9 + cols], block_rows=block_rows, transposed=True)
+    wq, ws = ol.quantize(x.float().cpu().numpy(), block_rows, False)
+    assert np.array_equal(_bytes(want[0]), wq) and np.array_equal(want[1].cpu().numpy(), ws)
+    for g, w in zip(got, want):
+        same = np.array_equal(_bytes(g), _bytes(w)) if g.dtype != F32 else torch.equal(g, w)
+        assert same
+
+
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("cols", [*range(1, 25), *range(120, 137), 1021, 2045, 4093, 4099, 8189, 16381])
 def test_norm_reads_no_column_past_the_row(cols, dtype):
