@@ -244,6 +244,19 @@ hipError_t launch_long_norm(const NormArgs &a, hipStream_t s) {
 template <typename T, Out OUT>
 hipError_t norm(const NormArgs &a, hipStream_t s) {
   if (a.cols < 8) return launch_long_norm<T, OUT>(a, s);  // shorter than a load
+  // Where twice the lanes would be little more than half used, three chunks a
+  // lane, if rows fill the card so (five waves a SIMD): 4000 x 9000 bfloat16 30
+  // us, 42 on 1024 lanes; 16384 x 2800 to e4m3 42 and 51; but 64 x 4519 5.7 and
+  // 4.8.  float32 to float32 is bound by memory either way.
+  if constexpr (sizeof(T) == 2 || OUT != kTensor) {
+    const auto three = [&](int64_t lanes) {
+      return a.cols > 2 * 8 * lanes && a.cols <= 3 * 8 * lanes && a.rows * lanes >= 256 * 1280;
+    };
+    if (three(64)) return launch_norm<T, OUT, 64, 3>(a, s);
+    if (three(128)) return launch_norm<T, OUT, 128, 3>(a, s);
+    if (three(256)) return launch_norm<T, OUT, 256, 3>(a, s);
+    if (three(512)) return launch_norm<T, OUT, 512, 3>(a, s);
+  }
   if (a.cols <= 128) return launch_norm<T, OUT, 16, 1>(a, s);
   if (a.cols <= 256) return launch_norm<T, OUT, 16, 2>(a, s);
   if (a.cols <= 512) return launch_norm<T, OUT, 64, 1>(a, s);

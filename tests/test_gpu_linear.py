@@ -479,6 +479,29 @@ def test_quantize_reads_nothing_past_the_matrix(rows, cols, dtype, block_rows):
         assert same
 
 
+@pytest.mark.parametrize("rows,cols", [(5200, 1025), (5121, 1536), (2600, 2049), (2561, 2900), (1300, 4097), (1281, 6144),
+                                       (700, 8193), (641, 12288)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_norm_of_many_rows(rows, cols, dtype):
+    """Many rows may take another split of a row over lanes, with another order
+    of a row's sums: against float64, the quantised form too."""
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    x = torch.randn(rows, cols, generator=gen, device=_dev()).to(dtype)
+    w, b = torch.randn(cols, generator=gen, device=_dev()), torch.randn(cols, generator=gen, device=_dev())
+    say(f"many rows {rows} {cols} {dtype}")
+    y, m, r = X.layer_norm(x, w, b, stats=True)
+    xd, wd, bd = x[::7].double().cpu().numpy(), w.double().cpu().numpy(), b.double().cpu().numpy()
+    want, mean, rstd = ol.layer_norm(xd, wd, bd, 1e-5)
+    _close(_np(y[::7]), want, _norm_tol(xd, wd, bd, want, rstd, dtype), "y")
+    q, s, m2, r2 = X.layer_norm_quantize(x, w, b, stats=True)
+    back = (q.float().cpu().double().numpy()[::7]
+            * np.repeat(s.cpu().double().numpy().T[::7], 128, axis=1)[:, :cols])
+    # half a step of e4m3, or of its subnormals, whose step is 2^-9 of the scale
+    step = np.repeat(s.cpu().double().numpy().T[::7], 128, axis=1)[:, :cols]
+    tol = _norm_tol(xd, wd, bd, want, rstd, F32) * 1.07
+    _close(back, want, tol + np.maximum((2.0 ** -4 + U32) * (np.abs(want) + tol), 2.0 ** -10 * step), "quantised")
+
+
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("cols", [*range(1, 25), *range(120, 137), 1021, 2045, 4093, 4099, 8189, 16381])
 def test_norm_reads_no_column_past_the_row(cols, dtype):
