@@ -117,7 +117,8 @@ int xpose_fp8_quantize(int64_t rows, int64_t cols, const void *x, int64_t ldx,
  * mean = sum x / cols and rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps), in
  * float32; y has x's dtype.  weight (NULL: ones) and bias (NULL: zeros) are
  * cols values of param_dtype.  mean and rstd (rows float32 values each) are
- * both given or both NULL.  eps >= 0.  y may be x itself (same pitch). */
+ * both given or both NULL.  eps >= 0.  y may be x itself (same pitch).  This
+ * and the next two: rows <= 2^31 - 1. */
 int xpose_layer_norm(int64_t rows, int64_t cols, const void *x, int64_t ldx,
                      int32_t dtype, const void *weight, const void *bias,
                      int32_t param_dtype, float eps, void *y, int64_t ldy,
