@@ -4,6 +4,7 @@
 // the smallest calls (one token, a handful of small gradients) take the GPU
 // 4 to 6 us, less than the same checks take in Python (14 and 41 us).
 
+#include <c10/core/StreamGuard.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -58,8 +59,9 @@ void same_device(const Tensor &first, const OptTensor &t) {
 }
 
 // The stream of a call: the current one of the tensors' device, or the
-// caller's.  Tensors allocated on the current stream but used on another are
-// kept from being reused before its work has run.
+// caller's.  On the caller's, everything that the call allocates comes from
+// that stream's memory: what the current stream's pool hands out may still be
+// in use by work queued there, which the call does not wait for.
 class Stream {
  public:
   Stream(const Tensor &t, const py::object &given) {
@@ -67,24 +69,38 @@ class Stream {
     if (t.device().index() != current)
       bad_value("tensors on " + t.device().str() + ", but the current device is cuda:" +
                 std::to_string(current));
-    if (given.is_none()) {
-      raw_ = c10::hip::getCurrentHIPStream(current).stream();
-    } else {
-      raw_ = reinterpret_cast<void *>(given.attr("cuda_stream").cast<uintptr_t>());
-      other_ = c10::Stream::unpack3(given.attr("stream_id").cast<int64_t>(),
-                                    (c10::DeviceIndex)given.attr("device_index").cast<int>(),
-                                    (c10::DeviceType)given.attr("device_type").cast<int>());
-    }
+    raw_ = c10::hip::getCurrentHIPStream(current).stream();
+    if (given.is_none()) return;
+    const auto other = c10::Stream::unpack3(given.attr("stream_id").cast<int64_t>(),
+                                            (c10::DeviceIndex)given.attr("device_index").cast<int>(),
+                                            (c10::DeviceType)given.attr("device_type").cast<int>());
+    if (other.device() != t.device())
+      bad_value("tensors on " + t.device().str() + ", but a stream of " + other.device().str());
+    raw_ = reinterpret_cast<void *>(given.attr("cuda_stream").cast<uintptr_t>());
+    guard_.emplace(other);
   }
   void *raw() const { return raw_; }
+  // The caller's tensors: kept from being reused before the call's work has run.
   template <typename... Ts>
-  void record(const Ts &...tensors) const {
-    if (other_) (..., (tensors.defined() ? tensors.record_stream(*other_) : void()));
+  void uses(const Ts &...tensors) const {
+    if (guard_) (..., record(tensors, guard_->current_stream()));
+  }
+  // Tensors that the call allocated and returns: the caller goes on with them
+  // on the stream that was current.
+  template <typename... Ts>
+  void returns(const Ts &...tensors) const {
+    if (guard_) (..., record(tensors, guard_->original_stream()));
   }
 
  private:
+  static void record(const Tensor &t, const c10::Stream &s) {
+    if (t.defined()) t.record_stream(s);
+  }
+  static void record(const OptTensor &t, const c10::Stream &s) {
+    if (t) record(*t, s);
+  }
   void *raw_ = nullptr;
-  std::optional<c10::Stream> other_;
+  std::optional<c10::StreamGuard> guard_;
 };
 
 struct Matrix {
@@ -167,7 +183,8 @@ Tensor fp8_gemm(const Tensor &a, const Tensor &scale_a, const Tensor &b, const T
                        scale_b.data_ptr<float>(), sb.ld, block_rows, out.data_ptr(), mc.ld, code, flags,
                        ws.defined() ? ws.data_ptr() : nullptr, info.workspace_bytes, on.raw()),
         "xpose_fp8_gemm");
-  on.record(a, scale_a, b, scale_b, ws, out);
+  on.uses(a, scale_a, b, scale_b, given);
+  if (!given) on.returns(out);
   return out;
 }
 
@@ -192,7 +209,8 @@ std::vector<Tensor> fp8_quantize(const Tensor &x, int64_t block_rows, bool pow2,
                              transposed ? scale_t.data_ptr<float>() : nullptr,
                              transposed ? scale_t.size(1) : 0, on.raw()),
           "xpose_fp8_quantize");
-  on.record(x, q, scale, qt, scale_t);
+  on.uses(x);
+  on.returns(q, scale, qt, scale_t);
   if (transposed) return {q, scale, qt, scale_t};
   return {q, scale};
 }
@@ -237,7 +255,9 @@ std::vector<Tensor> layer_norm(const Tensor &x, const OptTensor &weight, const O
                          out.data_ptr(), my.ld, stats ? mean.data_ptr<float>() : nullptr,
                          stats ? rstd.data_ptr<float>() : nullptr, on.raw()),
         "xpose_layer_norm");
-  on.record(x, out, mean, rstd, weight.value_or(Tensor()), bias.value_or(Tensor()));
+  on.uses(x, weight, bias, given);
+  on.returns(mean, rstd);
+  if (!given) on.returns(out);
   if (stats) return {out, mean, rstd};
   return {out};
 }
@@ -259,7 +279,8 @@ std::vector<Tensor> layer_norm_quantize(const Tensor &x, const OptTensor &weight
                                   std::max<int64_t>(mx.rows, 1), stats ? mean.data_ptr<float>() : nullptr,
                                   stats ? rstd.data_ptr<float>() : nullptr, on.raw()),
         "xpose_layer_norm_quantize");
-  on.record(x, q, scale, mean, rstd, weight.value_or(Tensor()), bias.value_or(Tensor()));
+  on.uses(x, weight, bias);
+  on.returns(q, scale, mean, rstd);
   if (stats) return {q, scale, mean, rstd};
   return {q, scale};
 }
@@ -287,7 +308,8 @@ std::tuple<Tensor, Tensor, Tensor> layer_norm_backward(const Tensor &dy, const T
                                   p.code, dx.data_ptr(), mx.cols, dweight.data_ptr<float>(), dbias.data_ptr<float>(),
                                   ws.data_ptr(), size, on.raw()),
         "xpose_layer_norm_backward");
-  on.record(dy, x, mean, rstd, ws, dx, dweight, dbias, weight.value_or(Tensor()));
+  on.uses(dy, x, mean, rstd, weight);
+  on.returns(dx, dweight, dbias);
   return {dx, dweight, dbias};
 }
 
@@ -331,7 +353,8 @@ py::tuple clip_grad_norm(const py::object &given_grads, double max_norm, double 
       if (g.numel() && o.strides() != g.strides()) bad_value("an output differs from its gradient in strides");
     }
     table[(size_t)i] = {g.data_ptr(), o.data_ptr(), g.numel(), code, 0};
-    on.record(g, o);
+    on.uses(g);
+    if (make) on.returns(o); else on.uses(o);
   }
   int64_t size = 0;
   check(xpose_clip_grad_norm_workspace(n, table.data(), &size), "xpose_clip_grad_norm_workspace");
@@ -340,7 +363,7 @@ py::tuple clip_grad_norm(const py::object &given_grads, double max_norm, double 
   check(xpose_clip_grad_norm(n, table.data(), max_norm, eps, norm.data_ptr<float>(),
                              size ? ws.data_ptr() : nullptr, size, on.raw()),
         "xpose_clip_grad_norm");
-  on.record(norm, ws);
+  on.returns(norm);
   return py::make_tuple(norm, make ? out : given_out);
 }
 

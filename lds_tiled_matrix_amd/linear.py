@@ -13,9 +13,11 @@ a float32 tensor with ceil(cols / 128) rows, one for each 128 columns of
 128 rows (``block_rows`` 128).  An element stands for q * scale.
 
 Every function takes ``stream``, a torch stream to run on instead of the
-current one.  Tensors must be on the current device.  Arguments that do not
-fit together raise ValueError, wrong dtypes TypeError, and what the library
-refuses (alignment, overlaps) XposeError, all before anything is launched.
+current one: nothing waits for the current one then, so the arguments have to
+be ready there, and what the call allocates comes from that stream's memory.
+Tensors must be on the current device.  Arguments that do not fit together
+raise ValueError, wrong dtypes TypeError, and what the library refuses
+(alignment, overlaps) XposeError, all before anything is launched.
 """
 from __future__ import annotations
 
