@@ -361,13 +361,43 @@ def _stream_handle(stream) -> int:
     return int(s.cuda_stream)
 
 
+def _torch_stream(stream):
+    import torch
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream.cuda_stream)
+
+
+def _empty(shape, like, stream, returned: bool = True):
+    """An uninitialised tensor of ``like``'s dtype and device for a call on
+    ``stream``, from that stream's memory: what the current stream's pool
+    hands out may still be in use by work queued there, which the call does
+    not wait for.  ``returned``: the caller goes on with it on the current
+    stream."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    with torch.cuda.stream(_torch_stream(stream)):
+        t = torch.empty(shape, dtype=like.dtype, device=like.device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _used_on(stream, *tensors) -> None:
+    """Keeps the caller's tensors from being reused before the call's work on
+    ``stream`` has run."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(_torch_stream(stream))
+
+
 def transpose(x, out=None, *, layout: int = LAYOUT_AUTO, tile=None,
               flags: int = 0, cache: int = CACHE_AUTO, group_rows: int = 0,
               order: int = ORDER_AUTO, persistent: int = 0, stream=None):
     """Transpose the last two dims of a 2-D or 3-D CUDA tensor whose last dim
     is contiguous.  Row pitches and the batch stride are taken from the
     tensor's strides.  Returns ``out`` (allocated contiguous if None)."""
-    import torch
     _require_device(x)
     if x.dim() not in (2, 3):
         raise ValueError("expected a 2-D or 3-D tensor")
@@ -377,7 +407,7 @@ def transpose(x, out=None, *, layout: int = LAYOUT_AUTO, tile=None,
     rows, cols = x.shape[-2], x.shape[-1]
     if out is None:
         shape = (cols, rows) if x.dim() == 2 else (batch, cols, rows)
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = _empty(shape, x, stream)
     _require_device(x, out)
     if out.dtype != x.dtype or out.stride(-1) != 1:
         raise ValueError("out must match dtype and have a contiguous last dim")
@@ -395,6 +425,7 @@ def transpose(x, out=None, *, layout: int = LAYOUT_AUTO, tile=None,
     _check(xpose_batched_ex(out.data_ptr(), x.data_ptr(), batch, rows, cols,
                             ld_in, ld_out, stride_in, stride_out, code, opts,
                             _stream_handle(stream)), "xpose_batched_ex")
+    _used_on(stream, x, out)
     return out
 
 
@@ -407,6 +438,7 @@ def copy(dst, src, stream=None):
         raise ValueError("byte sizes differ")
     _check(xpose_copy(dst.data_ptr(), src.data_ptr(), nbytes,
                       _stream_handle(stream)), "xpose_copy")
+    _used_on(stream, dst, src)
     return dst
 
 
@@ -451,7 +483,7 @@ def sgemm(a, b, c=None, *, alpha: float = 1.0, beta: float = 0.0,
     if c is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs c")
-        c = torch.empty((m, n), dtype=torch.float32, device=a.device)
+        c = _empty((m, n), a, stream)
     for t in (a, b, c):
         if t.dtype != torch.float32 or (t.numel() > 1 and t.stride(-1) != 1):
             raise ValueError("float32 tensors with a contiguous last dim")
@@ -467,17 +499,13 @@ def sgemm(a, b, c=None, *, alpha: float = 1.0, beta: float = 0.0,
         _check(rc, "xpose_sgemm_plan_ws")
     ws = None
     if info.workspace_wanted:
-        ws = torch.empty(info.workspace_wanted // 4, dtype=torch.float32,
-                         device=a.device)
+        ws = _empty(info.workspace_wanted // 4, a, stream, returned=False)
     _check(xpose_sgemm_ws(m, n, k, alpha, a.data_ptr(), lda, b.data_ptr(),
                           ldb, beta, c.data_ptr(), ldc, opts,
                           ws.data_ptr() if ws is not None else 0,
                           info.workspace_wanted, _stream_handle(stream)),
            "xpose_sgemm_ws")
-    if ws is not None and stream is not None:
-        # allocated on the current stream, used on `stream`: keep it from
-        # being reused before the call's kernels have run there
-        ws.record_stream(stream)
+    _used_on(stream, a, b, c)
     return c
 
 
