@@ -86,10 +86,12 @@ typedef struct xpose_fp8_gemm_info {
  * lies under 2^-13 of the largest one's leading bit, at most 2^-10 of the
  * products' magnitudes (1.4e-5 of the result's norm on normal data, where
  * bfloat16's rounding is 1.6e-3).  For float32 the products are summed in
- * full, at half the rate.  k == 0 gives zeros.  A workspace lets few tiles with a long k run as several
- * slices; xpose_fp8_gemm_plan says how many bytes (0: none needed); with
- * less, the call fails with XPOSE_EWORKSPACE.  The workspace is 16-byte
- * aligned.  a and b may overlap. */
+ * full, at half the rate.  A block's sum takes one scale after the other, each
+ * step in float32: while scales lie between 2^-100 and 2^100 (or are 0) nothing
+ * is lost to that, whatever their product.  k == 0 gives zeros.  A workspace
+ * lets few tiles with a long k run as several slices; xpose_fp8_gemm_plan says
+ * how many bytes (0: none needed); with less, the call fails with
+ * XPOSE_EWORKSPACE.  The workspace is 16-byte aligned.  a and b may overlap. */
 int xpose_fp8_gemm(int64_t m, int64_t n, int64_t k, const void *a, int64_t lda,
                    const float *scale_a, int64_t ld_scale_a, const void *b,
                    int64_t ldb, const float *scale_b, int64_t ld_scale_b,

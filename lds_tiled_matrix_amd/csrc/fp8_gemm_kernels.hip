@@ -3,8 +3,8 @@
 //
 // v_mfma_f32_16x16x128_f8f6f4 takes one whole block of 128 products of 16 x
 // 16 outputs: it starts from zero, and its float32 result is then scaled by
-// scale_a scale_b into the sum (kFp8Rows, kFp8Tiles: one multiply-add an
-// output and block; with a scale of b for each row a multiplication more).
+// scale_a scale_b into the sum (kFp8Tiles: one multiply-add an output and block;
+// kFp8Rows, with a scale of b for each row: a multiplication more).
 // Scales that are powers of two go into the instruction itself, which adds
 // straight to the sum (kFp8Pow2).
 //
@@ -18,6 +18,14 @@
 // every e4m3 value, and v_mfma_f32_16x16x32_bf16 multiplies them at half the
 // rate, with 4e-8 to 2e-7 of the norm on the same data.  Powers of two are
 // then scaled by like other scales.
+//
+// Scales.  The product of two scales may leave float32's range where the result
+// does not (2^-70 and 2^-70 next to sums of 2^20, or 2^70 and 2^70 next to a sum
+// of 0), so it is not formed: a block's result takes one scale after the other.
+// A scale of b that holds for all of a wave's columns (kFp8Tiles) has its power
+// of two applied by the instruction, or in the widening, and the rest goes to
+// a's scale, for one multiply-add an output still (with another multiplication
+// 4096^3 took 73 instead of 68 us, 8192^3 531 instead of 487).
 //
 // b's rows are the instruction's first operand, so a lane's four results are
 // neighbours in a row of c.  Which 128 bytes of a row are which of the
@@ -44,21 +52,22 @@ constexpr int kBlock = 128;
 template <bool EXACT> struct Lane32;
 template <> struct Lane32<false> {
   i32x8 v;
-  __device__ void set(u32x4 lo, u32x4 hi) {
+  __device__ void set(u32x4 lo, u32x4 hi, float = 1.f) {
     v = i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
               (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
   }
 };
 template <> struct Lane32<true> {
   bf16x8 v[4];
-  __device__ void set(u32x4 lo, u32x4 hi) {
+  // `power`, of two, is multiplied by.
+  __device__ void set(u32x4 lo, u32x4 hi, float power = 1.f) {
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
       const uint32_t bytes = w < 4 ? lo[w % 4] : hi[w % 4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const bf16x2 r = h ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(bytes, 1.f, true)
-                           : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(bytes, 1.f, false);
+        const bf16x2 r = h ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(bytes, power, true)
+                           : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(bytes, power, false);
         v[w / 2][w % 2 * 4 + 2 * h] = r[0];
         v[w / 2][w % 2 * 4 + 2 * h + 1] = r[1];
       }
@@ -71,6 +80,20 @@ template <> struct Lane32<true> {
 __device__ inline int exponent_of(float scale) {
   return (int)(__float_as_uint(scale) >> 23);
 }
+
+// A scale, the same in all lanes of a wave, as a power of two and the rest, of
+// magnitude 1 to 2.  What has no such power (zeros and what lies under float32's
+// normal numbers, inf, NaN) is rest.
+struct SplitScale {
+  float power, rest;
+  __device__ explicit SplitScale(float scale) {
+    const uint32_t bits = (uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(scale));
+    const uint32_t exponent = bits & 0x7f800000u;
+    const bool none = exponent == 0 || exponent == 0x7f800000u;
+    power = none ? 1.f : __uint_as_float(exponent);
+    rest = __uint_as_float(none ? bits : (bits & 0x807fffffu) | 0x3f800000u);
+  }
+};
 
 __device__ inline f32x4 multiply(const Lane32<false> &b, const Lane32<false> &a) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
@@ -188,8 +211,8 @@ __device__ inline void reads_and_barrier() {
 // What bounds it: at 256 x 256 a block of k reads 192 KiB of LDS and writes 64,
 // which at 128 bytes a cycle are the 2,048 cycles of its products, so both run
 // full; 8192^3 takes 410 to 420 us with powers of two (2.6 PFLOP/s, the clock
-// down to 1.9 GHz), 470 with tile scales and 524 with row scales, whose
-// multiply-adds take turns with the products.  The exact kernels (128 x 128, two
+// down to 1.9 GHz), 480 to 490 with tile scales and 530 to 550 with row scales,
+// whose multiply-adds take turns with the products.  The exact kernels (128 x 128, two
 // workgroups on a compute unit) spend as many cycles on widening and scaling as
 // on products: 4096^3 takes 130 us (1.06 PFLOP/s).
 //
@@ -358,7 +381,7 @@ __global__ __launch_bounds__((Tile<TM, TN, WM>::THREADS), 2) void fp8_tile_kerne
     v.lo = *reinterpret_cast<const u32x4 *>(buf + (place_b + lo) + j * 16 * kBlock);
     v.hi = *reinterpret_cast<const u32x4 *>(buf + (place_b + hi) + j * 16 * kBlock);
     if constexpr (MODE == kFp8Pow2) v.scale = *reinterpret_cast<const float *>(buf + place_sb + j / 2 * 128 + j % 2 * 16);
-    if constexpr (MODE == kFp8Tiles) v.scale = *reinterpret_cast<const float *>(buf + place_sb);
+    if (MODE == kFp8Tiles && j == 0) v.scale = *reinterpret_cast<const float *>(buf + place_sb);
     if constexpr (MODE == kFp8Rows) v.scales = *reinterpret_cast<const f32x4 *>(buf + place_sb + j / 2 * 128 + j % 2 * 16);
     return v;
   };
@@ -392,8 +415,10 @@ __global__ __launch_bounds__((Tile<TM, TN, WM>::THREADS), 2) void fp8_tile_kerne
     auto add = [&](f32x4 &sum) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        sum[e] = __builtin_fmaf(last[e], MODE == kFp8Rows ? last_s1 * last_s2[e] : last_s1, sum[e]);
+        sum[e] = MODE == kFp8Rows ? __builtin_fmaf(last[e] * last_s1, last_s2[e], sum[e])
+                                  : __builtin_fmaf(last[e], last_s1, sum[e]);
     };
+    const SplitScale of_b(MODE == kFp8Tiles ? b.scale : 1.f);
     Lane32<EXACT> al[T::NI];
 #pragma unroll
     for (int i = 0; i < T::NI; ++i) al[i].set(a[i].lo, a[i].hi);
@@ -401,7 +426,7 @@ __global__ __launch_bounds__((Tile<TM, TN, WM>::THREADS), 2) void fp8_tile_kerne
     for (int j = 0; j < T::NJ; ++j) {
       const Rows16 now = b;
       Lane32<EXACT> bl;
-      bl.set(now.lo, now.hi);
+      bl.set(now.lo, now.hi, of_b.power);
       if (j + 1 < T::NJ) {
         b = read_b(buf, j + 1);
       } else if constexpr (MORE) {
@@ -420,11 +445,15 @@ __global__ __launch_bounds__((Tile<TM, TN, WM>::THREADS), 2) void fp8_tile_kerne
           acc[i][j] = multiply(bl, al[i], acc[i][j], exponent_of(now.scale), exponent_of(a[i].scale));
         } else {
           // Each product is added in behind the next one's start, not waited for.
-          const f32x4 v = multiply(bl, al[i]);
+          f32x4 v;
+          if constexpr (MODE == kFp8Tiles && !EXACT)
+            v = multiply(bl, al[i], f32x4{0.f, 0.f, 0.f, 0.f}, exponent_of(of_b.power), exponent_of(1.f));
+          else
+            v = multiply(bl, al[i]);
           if (i > 0) add(acc[i - 1][j]);
           else if (j > 0) add(acc[T::NI - 1][j - 1]);
           last = v;
-          last_s1 = MODE == kFp8Tiles ? a[i].scale * now.scale : a[i].scale;
+          last_s1 = MODE == kFp8Tiles ? a[i].scale * of_b.rest : a[i].scale;
           last_s2 = now.scales;
         }
         if (MORE && j + 1 == T::NJ) {
@@ -549,7 +578,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void fp8_skinny_kernel(Fp8GemmAr
         const f32x4 v = multiply(bl, al);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          acc[i][e] = __builtin_fmaf(v[e], sav[d][i] * sbv[d][e], acc[i][e]);
+          acc[i][e] = __builtin_fmaf(v[e] * sav[d][i], sbv[d][e], acc[i][e]);
       }
     }
   }
