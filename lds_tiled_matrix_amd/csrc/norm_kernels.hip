@@ -333,9 +333,16 @@ __global__ __launch_bounds__(norm_threads(TR)) void norm_bwd_kernel(NormBwdArgs 
     fetch(row + groups < a.rows ? row + groups : row);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
+      const int valid = in_row(a.cols, (i * TR + lane) * 8);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[i][e] = (x[i][e] - mean) * rstd;
+      if (valid < 8) {  // a dy of 0 beyond the row is not enough: -mean rstd may be inf
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e >= valid) x[i][e] = 0.f;
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[i][e] = (x[i][e] - mean) * rstd;  // times a dy of 0 beyond the row
         const float g = dy[i][e] * w[i][e];
         s1 += g;
         s2 = __builtin_fmaf(g, x[i][e], s2);
@@ -430,7 +437,7 @@ __global__ __launch_bounds__(kLongThreads) void norm_bwd_sums_kernel(NormBwdArgs
     for (int e = 0; e < 8; ++e) {
       const float g = dy[e] * w[e];
       t1 += g;
-      t2 = __builtin_fmaf(g, (x[e] - mean) * rstd, t2);
+      t2 = __builtin_fmaf(g, e < valid ? (x[e] - mean) * rstd : 0.f, t2);
     }
     s1 += t1;
     s2 += t2;
