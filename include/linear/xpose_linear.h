@@ -35,7 +35,9 @@
  *
  * Errors (validated on the host before anything is launched):
  *   XPOSE_EINVAL  a negative size, a pitch below its row, a NULL pointer that
- *                 the call would use, an extent that overflows, unknown flags
+ *                 the call would use, an extent that overflows, unknown flags,
+ *                 a size that one launch of 2^32 - 1 threads cannot cover
+ *                 (stated per call)
  *   XPOSE_EDTYPE  a dtype that is not XPOSE_F32, XPOSE_F16 or XPOSE_BF16
  *   XPOSE_EALIGN  a pointer off its element's size (stated per call where
  *                 more is needed)
@@ -91,7 +93,8 @@ typedef struct xpose_fp8_gemm_info {
  * is lost to that, whatever their product.  k == 0 gives zeros.  A workspace
  * lets few tiles with a long k run as several slices; xpose_fp8_gemm_plan says
  * how many bytes (0: none needed); with less, the call fails with
- * XPOSE_EWORKSPACE.  The workspace is 16-byte aligned.  a and b may overlap. */
+ * XPOSE_EWORKSPACE.  The workspace is 16-byte aligned.  a and b may overlap.
+ * ceil(m / 128) ceil(n / 128) < 2^24. */
 int xpose_fp8_gemm(int64_t m, int64_t n, int64_t k, const void *a, int64_t lda,
                    const float *scale_a, int64_t ld_scale_a, const void *b,
                    int64_t ldb, const float *scale_b, int64_t ld_scale_b,
@@ -108,7 +111,7 @@ int xpose_fp8_gemm_plan(int64_t m, int64_t n, int64_t k, int32_t b_block_rows,
 /* Quantises x (rows x cols, pitch ldx, of dtype) into q and scale, and, where
  * qt is not NULL, its transpose (cols x rows) into qt and scale_t, in one
  * pass over x.  block_rows: 1 or 128, of both.  q and qt are 8-byte aligned
- * with ldq and ldqt multiples of 8. */
+ * with ldq and ldqt multiples of 8.  ceil(rows / 128) ceil(cols / 128) < 2^24. */
 int xpose_fp8_quantize(int64_t rows, int64_t cols, const void *x, int64_t ldx,
                        int32_t dtype, int32_t block_rows, int32_t flags,
                        void *q, int64_t ldq, float *scale, int64_t ld_scale,
@@ -142,7 +145,8 @@ int xpose_layer_norm_quantize(int64_t rows, int64_t cols, const void *x,
  *   dbias   = sum over rows of dy           (NULL: not wanted)
  *
  * dy, x and dx are of dtype; dweight and dbias are `cols` float32 values,
- * zeros when there are no rows.  dx may be dy itself (same pitch). */
+ * zeros when there are no rows.  dx may be dy itself (same pitch).  Over 8192
+ * columns: ceil(cols / 2048) min(rows, 256) < 2^24. */
 int xpose_layer_norm_backward(int64_t rows, int64_t cols, const void *dy,
                               int64_t lddy, const void *x, int64_t ldx,
                               int32_t dtype, const float *mean,

@@ -19,7 +19,7 @@ using xpose::record_hip_error;
 
 constexpr int64_t kBlock = 128;
 constexpr int64_t kMaxFp8Pitch = ((int64_t)1 << 23) - 16;
-constexpr int64_t kMaxGrid = INT32_MAX;
+constexpr int64_t kMaxRows = INT32_MAX;
 
 int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b != 0); }
 
@@ -140,12 +140,11 @@ int plan_gemm(int64_t m, int64_t n, int64_t k, int out_dtype, GemmPlan &plan) {
     if (kern.exact != exact || (kern.skinny && kern.tile_m != skinny_rows)) continue;
     const int64_t tiles_m = ceil_div(m, kern.tile_m), tiles_n = ceil_div(n, kern.tile_n);
     int64_t tiles;
-    if (__builtin_mul_overflow(tiles_m, tiles_n, &tiles) || tiles > kMaxGrid / kMaxSplits)
-      continue;
+    if (__builtin_mul_overflow(tiles_m, tiles_n, &tiles)) continue;
     const int64_t most = kern.tile_m == 256 ? 1 : kMaxSplits;
     for (int64_t want = 1; want <= most && want <= blocks; ++want) {
       const int64_t per = ceil_div(blocks, want), splits = ceil_div(blocks, per);
-      if (splits != want) continue;
+      if (splits != want || tiles > xpose::kMaxThreads / kern.threads / splits) continue;
       int64_t bytes = 0;
       if (splits > 1 && (__builtin_mul_overflow(m, n, &bytes) ||
                          __builtin_mul_overflow(bytes, 4 * splits, &bytes)))
@@ -280,7 +279,9 @@ int xpose_fp8_quantize(int64_t rows, int64_t cols, const void *x, int64_t ldx,
   if (!size) return XPOSE_EDTYPE;
   const int64_t tiles_r = ceil_div(rows, kBlock), tiles_c = ceil_div(cols, kBlock);
   int64_t tiles;
-  if (__builtin_mul_overflow(tiles_r, tiles_c, &tiles) || tiles > kMaxGrid) return XPOSE_EINVAL;
+  if (__builtin_mul_overflow(tiles_r, tiles_c, &tiles) ||
+      tiles > xpose::kMaxThreads / xpose::kQuantThreads)
+    return XPOSE_EINVAL;
   Ranges r;
   r.matrix(x, rows, cols, ldx, size, size, false);
   r.matrix(q, rows, cols, ldq, 1, 8, true);
@@ -317,7 +318,7 @@ static int layer_norm(int64_t rows, int64_t cols, const void *x, int64_t ldx,
                       int32_t param_dtype, float eps, bool quantized,
                       int32_t flags, void *y, int64_t ldy, float *scale,
                       int64_t ld_scale, float *mean, float *rstd, void *stream) {
-  if (rows < 0 || cols < 0 || rows > kMaxGrid || (flags & ~XPOSE_LINEAR_POW2) ||
+  if (rows < 0 || cols < 0 || rows > kMaxRows || (flags & ~XPOSE_LINEAR_POW2) ||
       !(eps >= 0) || (mean == nullptr) != (rstd == nullptr))
     return XPOSE_EINVAL;
   const int size = size_of(dtype), param = size_of(param_dtype);
@@ -387,7 +388,7 @@ static int bwd_floats(int64_t rows, int64_t cols, int64_t *floats) {
 }
 
 int xpose_layer_norm_backward_workspace(int64_t rows, int64_t cols, int64_t *bytes) {
-  if (rows < 0 || cols < 0 || rows > kMaxGrid || !bytes) return XPOSE_EINVAL;
+  if (rows < 0 || cols < 0 || rows > kMaxRows || !bytes) return XPOSE_EINVAL;
   int64_t floats = 0;
   const int rc = bwd_floats(rows, cols, &floats);
   if (rc == XPOSE_OK) *bytes = 4 * floats;
@@ -401,16 +402,13 @@ int xpose_layer_norm_backward(int64_t rows, int64_t cols, const void *dy,
                               int32_t param_dtype, void *dx, int64_t lddx,
                               float *dweight, float *dbias, void *workspace,
                               int64_t workspace_bytes, void *stream) {
-  if (rows < 0 || cols < 0 || rows > kMaxGrid || workspace_bytes < 0) return XPOSE_EINVAL;
+  if (rows < 0 || cols < 0 || rows > kMaxRows || workspace_bytes < 0) return XPOSE_EINVAL;
   const int size = size_of(dtype), param = size_of(param_dtype);
   if (!size || !param) return XPOSE_EDTYPE;
   int64_t floats = 0;
   int rc = bwd_floats(rows, cols, &floats);
   if (rc != XPOSE_OK) return rc;
-  // the long-row kernels' grid
-  if (ceil_div(cols, 64) > kMaxGrid / 2 ||
-      (cols > 0 && xpose::norm_bwd_parts(rows, cols) > kMaxGrid / ceil_div(cols, 2048)))
-    return XPOSE_EINVAL;
+  if (!xpose::norm_bwd_fits(rows, cols)) return XPOSE_EINVAL;
   Ranges r;
   r.matrix(dy, rows, cols, lddy, size, size, false);
   r.matrix(x, rows, cols, ldx, size, size, false);

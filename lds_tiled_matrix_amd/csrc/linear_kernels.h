@@ -8,6 +8,8 @@
 
 namespace xpose {
 
+constexpr int64_t kMaxThreads = UINT32_MAX;  // of a launch
+
 // ----- matrix product (fp8_gemm_kernels.hip) --------------------------------
 
 struct Fp8GemmArgs {
@@ -51,6 +53,7 @@ struct QuantizeArgs {
   int64_t rows, cols, ldx, ldq, ld_scale, ldqt, ld_scale_t;
   uint32_t tiles_r, tiles_c;
 };
+constexpr int kQuantThreads = 256;  // of the workgroup that each tile takes
 hipError_t launch_quantize(const QuantizeArgs &, int dtype, int block_rows,
                            bool pow2, hipStream_t);
 
@@ -101,6 +104,9 @@ struct NormBwdArgs {
 // How many partial sums of `cols` values the backward pass of these sizes
 // takes, and how many floats of row sums before them.
 int norm_bwd_parts(int64_t rows, int64_t cols);
+// Whether its launches are possible: rows of many columns take a workgroup for
+// each block of them and partial sum.
+bool norm_bwd_fits(int64_t rows, int64_t cols);
 int64_t norm_bwd_row_floats(int64_t rows, int64_t cols);
 hipError_t launch_layer_norm_backward(const NormBwdArgs &, int dtype,
                                       hipStream_t);

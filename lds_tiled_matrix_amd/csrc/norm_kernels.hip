@@ -167,13 +167,23 @@ __global__ __launch_bounds__(norm_threads(TR)) void norm_kernel(NormArgs a) {
   }
 }
 
+// A workgroup of 1024 for each of `count` things.  A launch can have no more than
+// 2^32 - 1 threads in one dimension, so past 4 million workgroups they go on in
+// the second; the last ones may have nothing to do.
+constexpr int kLongThreads = 1024;
+dim3 long_grid(int64_t count, uint32_t kinds = 1) {
+  const int64_t most = kMaxThreads / kLongThreads, x = count < most ? count : most;
+  return dim3((uint32_t)x, (uint32_t)((count + x - 1) / x), kinds);
+}
+__device__ inline int64_t long_index() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // Rows of any length, in three sweeps; the second and third find much of the
 // row in the caches.
-constexpr int kLongThreads = 1024;
 template <typename T, Out OUT>
 __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(NormArgs a) {
   __shared__ float lds[2][kLongThreads / 64];
-  const int64_t row = blockIdx.x;
+  const int64_t row = long_index();
+  if (row >= a.rows) return;
   const T *x = (const T *)a.x + row * a.ldx;
   constexpr int64_t kStep = kLongThreads * 8;
   float s = 0.f;
@@ -218,10 +228,10 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(NormArgs a) {
   }
 }
 
-hipError_t launch(const void *kernel, const NormArgs &a, uint32_t grid, int threads, hipStream_t s) {
+hipError_t launch(const void *kernel, const NormArgs &a, dim3 grid, int threads, hipStream_t s) {
   NormArgs copy = a;
   void *args[] = {&copy};
-  return hipLaunchKernel(kernel, dim3(grid), dim3(threads), args, 0, s);
+  return hipLaunchKernel(kernel, grid, dim3(threads), args, 0, s);
 }
 template <typename T, Out OUT, int TR, int NC>
 hipError_t launch_norm(const NormArgs &a, hipStream_t s) {
@@ -234,12 +244,12 @@ hipError_t launch_norm(const NormArgs &a, hipStream_t s) {
     return hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, norm_threads(TR), 0) == hipSuccess && n > 0 ? n : 1;
   }();
   const int64_t grid = (a.rows + per - 1) / per, most = 256 * (int64_t)at_once;
-  return launch(kernel, a, (uint32_t)(grid < most ? grid : most), norm_threads(TR), s);
+  return launch(kernel, a, dim3((uint32_t)(grid < most ? grid : most)), norm_threads(TR), s);
 }
 template <typename T, Out OUT>
 hipError_t launch_long_norm(const NormArgs &a, hipStream_t s) {
   return launch(reinterpret_cast<const void *>(&norm_long_kernel<T, OUT>), a,
-                (uint32_t)a.rows, kLongThreads, s);
+                long_grid(a.rows), kLongThreads, s);
 }
 template <typename T, Out OUT>
 hipError_t norm(const NormArgs &a, hipStream_t s) {
@@ -424,7 +434,8 @@ __global__ __launch_bounds__(norm_threads(TR)) void norm_bwd_kernel(NormBwdArgs 
 template <typename T>
 __global__ __launch_bounds__(kLongThreads) void norm_bwd_sums_kernel(NormBwdArgs a) {
   __shared__ float lds[2][kLongThreads / 64];
-  const int64_t row = blockIdx.x;
+  const int64_t row = long_index();
+  if (row >= a.rows) return;
   const float mean = a.mean[row], rstd = a.rstd[row];
   float s1 = 0.f, s2 = 0.f;
   for (int64_t col = threadIdx.x * 8; col < a.cols; col += kLongThreads * 8) {
@@ -450,9 +461,9 @@ __global__ __launch_bounds__(kLongThreads) void norm_bwd_sums_kernel(NormBwdArgs
   }
 }
 
-constexpr int kLongBlock = 2048;  // columns of a workgroup of 256
+constexpr int kLongBlockThreads = 256, kLongBlock = 8 * kLongBlockThreads;  // columns of a workgroup
 template <typename T>
-__global__ __launch_bounds__(256) void norm_bwd_long_kernel(NormBwdArgs a) {
+__global__ __launch_bounds__(kLongBlockThreads) void norm_bwd_long_kernel(NormBwdArgs a) {
   const int64_t blocks = (a.cols + kLongBlock - 1) / kLongBlock;
   const int64_t col = (int64_t)(blockIdx.x % blocks) * kLongBlock + threadIdx.x * 8;
   const int group = (int)(blockIdx.x / blocks);
@@ -481,15 +492,14 @@ __global__ __launch_bounds__(256) void norm_bwd_long_kernel(NormBwdArgs a) {
 
 // 64 columns of one gradient a workgroup: lane l of a wave has column l, the
 // 16 waves every 16th partial sum.
-constexpr int kParamWaves = 16;
+constexpr int kParamWaves = kLongThreads / 64;
 __global__ __launch_bounds__(64 * kParamWaves) void norm_bwd_params_kernel(NormBwdArgs a) {
   __shared__ float lds[kParamWaves][64];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int64_t blocks = (a.cols + 63) / 64;
-  const int which = blockIdx.x >= blocks;
-  const int64_t col = (int64_t)(blockIdx.x - which * blocks) * 64 + lane;
+  const int which = blockIdx.z;
+  const int64_t block = long_index(), col = block * 64 + lane;
   float *out = which ? a.dbias : a.dweight;
-  if (!out) return;
+  if (!out || block * 64 >= a.cols) return;
   float s = 0.f;
   if (col < a.cols) {
     const float *p = a.partial + which * a.cols + col;
@@ -508,23 +518,24 @@ __global__ __launch_bounds__(64 * kParamWaves) void norm_bwd_params_kernel(NormB
 // More than 8192 columns would spill registers, under eight are less than a load.
 constexpr bool in_registers(int64_t cols) { return cols >= 8 && cols <= 8192; }
 
-hipError_t launch(const void *kernel, const NormBwdArgs &a, int64_t grid, int threads, hipStream_t s) {
+hipError_t launch(const void *kernel, const NormBwdArgs &a, dim3 grid, int threads, hipStream_t s) {
   NormBwdArgs copy = a;
   void *args[] = {&copy};
-  return hipLaunchKernel(kernel, dim3((uint32_t)grid), dim3(threads), args, 0, s);
+  return hipLaunchKernel(kernel, grid, dim3(threads), args, 0, s);
 }
 template <typename T, int TR, int NC>
 hipError_t launch_bwd(const NormBwdArgs &a, hipStream_t s) {
   return launch(reinterpret_cast<const void *>(&norm_bwd_kernel<T, TR, NC>), a,
-                a.parts, norm_threads(TR), s);
+                dim3((uint32_t)a.parts), norm_threads(TR), s);
 }
 template <typename T>
 hipError_t norm_bwd(const NormBwdArgs &a, hipStream_t s) {
   if (!in_registers(a.cols)) {
-    hipError_t e = launch(reinterpret_cast<const void *>(&norm_bwd_sums_kernel<T>), a, a.rows, kLongThreads, s);
+    hipError_t e = launch(reinterpret_cast<const void *>(&norm_bwd_sums_kernel<T>), a, long_grid(a.rows),
+                          kLongThreads, s);
     if (e != hipSuccess) return e;
     return launch(reinterpret_cast<const void *>(&norm_bwd_long_kernel<T>), a,
-                  (a.cols + kLongBlock - 1) / kLongBlock * a.parts, 256, s);
+                  dim3((uint32_t)((a.cols + kLongBlock - 1) / kLongBlock * a.parts)), kLongBlockThreads, s);
   }
   if (a.cols <= 128) return launch_bwd<T, 16, 1>(a, s);
   if (a.cols <= 256) return launch_bwd<T, 16, 2>(a, s);
@@ -564,6 +575,11 @@ int norm_bwd_parts(int64_t rows, int64_t cols) {
   while (parts < most && parts * parts < 32 * rows) parts *= 2;
   return (int)(rows < parts ? rows : parts);
 }
+bool norm_bwd_fits(int64_t rows, int64_t cols) {
+  if (in_registers(cols)) return true;
+  const int64_t blocks = cols / kLongBlock + (cols % kLongBlock != 0);
+  return blocks == 0 || norm_bwd_parts(rows, cols) <= kMaxThreads / kLongBlockThreads / blocks;
+}
 int64_t norm_bwd_row_floats(int64_t rows, int64_t cols) {
   return in_registers(cols) ? 0 : 2 * rows;
 }
@@ -579,7 +595,7 @@ hipError_t launch_layer_norm_backward(const NormBwdArgs &a, int dtype, hipStream
   NormBwdArgs sums = a;
   if (a.rows > 0) sums.partial += norm_bwd_row_floats(a.rows, a.cols);
   return launch(reinterpret_cast<const void *>(&norm_bwd_params_kernel), sums,
-                2 * ((a.cols + 63) / 64), 64 * kParamWaves, s);
+                long_grid((a.cols + 63) / 64, 2), kLongThreads, s);
 }
 
 }  // namespace xpose

@@ -30,7 +30,6 @@ namespace {
 // 8192 x 8192 bfloat16 both ways takes 54 us (4.9 TB/s), 12345 x 6789 float32
 // 90 us (5.6 TB/s); a copy of as many bytes, 43 and 80.
 constexpr int kTile = 128;
-constexpr int kQuantThreads = 256;
 
 template <typename T, int BLOCK_ROWS, bool POW2, bool BOTH>
 __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(QuantizeArgs a) {
