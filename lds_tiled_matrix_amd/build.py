@@ -1,5 +1,5 @@
 """Build libxpose.so for gfx950 in-tree, and _linear.so, the torch side of
-linear.py, which is host code and built where torch is installed.
+linear.py, which is host code and built where a torch with HIP is installed.
 
     python lds_tiled_matrix_amd/build.py
 
@@ -72,13 +72,16 @@ def build(verbose: bool = False) -> str:
 
 
 def build_torch(verbose: bool = False) -> str | None:
-    """The Python extension over libxpose.so that takes torch tensors."""
+    """The Python extension over libxpose.so that takes torch tensors; None
+    where torch is not installed or has no HIP."""
     import importlib.util
     import sysconfig
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.origin:
         return None
     torch_dir = os.path.dirname(spec.origin)
+    if not os.path.exists(os.path.join(torch_dir, "lib", "libc10_hip.so")):
+        return None
     inc = os.path.join(torch_dir, "include")
     rocm = os.path.dirname(os.path.dirname(hipcc()))
     tmp = TORCH_LIB + ".tmp"

@@ -85,23 +85,23 @@ _bind(_lib)
 _check = _base._check
 
 
-def _load_native():
-    """_linear.so, the torch side of these functions (csrc/linear_torch.cpp).
-    Without torch there is nothing for it to do; with torch it must be
-    there."""
-    try:
-        import torch  # noqa: F401
-    except ImportError:
-        return None
-    try:
-        from . import _linear
-    except ImportError as e:
-        raise ImportError(f"{_base._HERE}/_linear.so is not built or does not fit this torch ({e}); "
-                          "run `python lds_tiled_matrix_amd/build.py`") from e
-    return _linear
+_native = None
 
 
-_native = _load_native()
+def _torch_side():
+    """_linear.so, the torch side of these functions (csrc/linear_torch.cpp),
+    loaded by the first call that needs it: the rest of the package does
+    without it."""
+    global _native
+    if _native is None:
+        import torch  # noqa: F401  (_linear.so takes its libraries from it)
+        try:
+            from . import _linear
+        except ImportError as e:
+            raise ImportError(f"{_base._HERE}/_linear.so is not built or does not fit this torch ({e}); "
+                              "run `python lds_tiled_matrix_amd/build.py`") from e
+        _native = _linear
+    return _native
 
 
 # ----- matrix product ----------------------------------------------------------
@@ -128,7 +128,7 @@ def fp8_gemm(a, scale_a, b, scale_b, *, out=None, out_dtype=None,
 
     ``pow2``: every scale is a power of two (made with ``pow2=True``), which
     the matrix cores then apply themselves."""
-    return _native.fp8_gemm(a, scale_a, b, scale_b, out, out_dtype, pow2, stream)
+    return _torch_side().fp8_gemm(a, scale_a, b, scale_b, out, out_dtype, pow2, stream)
 
 
 # ----- quantisation --------------------------------------------------------------
@@ -139,7 +139,7 @@ def fp8_quantize(x, *, block_rows: int = 1, pow2: bool = False,
     ``transposed`` (q, scale, qt, scale_t), the latter two of x.T, from one
     pass over x.  ``block_rows`` 1: a scale for each row and 128 columns (in
     each direction); 128: one for each 128 x 128 tile."""
-    return tuple(_native.fp8_quantize(x, block_rows, pow2, transposed, stream))
+    return tuple(_torch_side().fp8_quantize(x, block_rows, pow2, transposed, stream))
 
 
 # ----- layer norm ------------------------------------------------------------------
@@ -150,7 +150,7 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5,
     (y, mean, rstd), what ``layer_norm_backward`` needs.  ``weight`` and
     ``bias`` (None: ones, zeros) are both float32 or both of a 16-bit type;
     y has x's dtype; ``out`` may be x."""
-    y = _native.layer_norm(x, weight, bias, eps, stats, out, stream)
+    y = _torch_side().layer_norm(x, weight, bias, eps, stats, out, stream)
     return tuple(y) if stats else y[0]
 
 
@@ -159,14 +159,14 @@ def layer_norm_quantize(x, weight=None, bias=None, *, eps: float = 1e-5,
     """Layer norm straight to a quantised matrix: (q, scale), or with
     ``stats`` (q, scale, mean, rstd).  The normalised values are quantised
     from float32, with a scale for each row and 128 columns."""
-    return tuple(_native.layer_norm_quantize(x, weight, bias, eps, pow2, stats, stream))
+    return tuple(_torch_side().layer_norm_quantize(x, weight, bias, eps, pow2, stats, stream))
 
 
 def layer_norm_backward(dy, x, mean, rstd, weight=None, *, stream=None):
     """(dx, dweight, dbias) of ``layer_norm(x, weight, bias, stats=True)``
     for the output's gradient dy.  dx has x's dtype; dweight and dbias are
     float32, the same bit for bit on every run."""
-    return _native.layer_norm_backward(dy, x, mean, rstd, weight, stream)
+    return _torch_side().layer_norm_backward(dy, x, mean, rstd, weight, stream)
 
 
 # ----- clipping ----------------------------------------------------------------------
@@ -178,9 +178,9 @@ def clip_grad_norm(grads, max_norm: float, *, eps: float = 1e-6, out=None,
     that stays on the GPU.  ``out``: tensors of the same dtypes, shapes and
     strides (None: new ones; ``grads`` itself: in place).  Every gradient is
     float32, float16 or bfloat16 and fills one stretch of memory."""
-    return _native.clip_grad_norm(grads, max_norm, eps, out, stream)
+    return _torch_side().clip_grad_norm(grads, max_norm, eps, out, stream)
 
 
 def _dense(t) -> bool:
     """Whether a gradient's elements fill one stretch of memory, in any order."""
-    return _native.is_dense(t)
+    return _torch_side().is_dense(t)
