@@ -138,6 +138,15 @@ Tensor empty_e4m3(int64_t rows, int64_t cols, const Tensor &like) {
   return pitch == cols ? q : q.narrow(1, 0, cols);
 }
 
+// A tensor of the caller's that the call writes: autograd sees that what it
+// saved of it is gone.  (Inference tensors have no versions.)
+void modified(const Tensor &t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void modified(const OptTensor &t) {
+  if (t) modified(*t);
+}
+
 int64_t blocks(int64_t n) { return (n + 127) / 128; }
 std::string shape(int64_t a, int64_t b) {
   return "(" + std::to_string(a) + ", " + std::to_string(b) + ")";
@@ -183,6 +192,7 @@ Tensor fp8_gemm(const Tensor &a, const Tensor &scale_a, const Tensor &b, const T
                        scale_b.data_ptr<float>(), sb.ld, block_rows, out.data_ptr(), mc.ld, code, flags,
                        ws.defined() ? ws.data_ptr() : nullptr, info.workspace_bytes, on.raw()),
         "xpose_fp8_gemm");
+  modified(given);
   on.uses(a, scale_a, b, scale_b, given);
   if (!given) on.returns(out);
   return out;
@@ -255,6 +265,7 @@ std::vector<Tensor> layer_norm(const Tensor &x, const OptTensor &weight, const O
                          out.data_ptr(), my.ld, stats ? mean.data_ptr<float>() : nullptr,
                          stats ? rstd.data_ptr<float>() : nullptr, on.raw()),
         "xpose_layer_norm");
+  modified(given);
   on.uses(x, weight, bias, given);
   on.returns(mean, rstd);
   if (!given) on.returns(out);
@@ -363,6 +374,7 @@ py::tuple clip_grad_norm(const py::object &given_grads, double max_norm, double 
   check(xpose_clip_grad_norm(n, table.data(), max_norm, eps, norm.data_ptr<float>(),
                              size ? ws.data_ptr() : nullptr, size, on.raw()),
         "xpose_clip_grad_norm");
+  for (Py_ssize_t i = 0; i < n && !make; ++i) modified(tensor_of(PySequence_Fast_GET_ITEM(out.ptr(), i), "out"));
   on.returns(norm);
   return py::make_tuple(norm, make ? out : given_out);
 }

@@ -18,6 +18,11 @@ be ready there, and what the call allocates comes from that stream's memory.
 Tensors must be on the current device.  Arguments that do not fit together
 raise ValueError, wrong dtypes TypeError, and what the library refuses
 (alignment, overlaps) XposeError, all before anything is launched.
+
+Nothing is recorded for autograd: results do not require gradients, whatever
+the arguments do, and ``layer_norm_backward`` and the products of transposed
+operands are called by hand (or from a torch.autograd.Function).  What a call
+writes to a tensor given as ``out`` counts as a change in place.
 """
 from __future__ import annotations
 
