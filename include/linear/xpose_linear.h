@@ -27,8 +27,9 @@
  * Memory and streams.  Pointers are DEVICE pointers on the current HIP device
  * unless a comment says host.  Sizes and pitches count elements.  Calls are
  * asynchronous on `stream` (NULL = the null stream), never synchronise, never
- * allocate, keep no state, record no memset or copy, and may be captured into
- * a graph.  A workspace is written and read by the call's own kernels only;
+ * allocate device memory, keep nothing of one call for the next (but how many
+ * workgroups of a kernel run at once, asked for once), record no memset or
+ * copy, and may be captured into a graph.  A workspace is written and read by the call's own kernels only;
  * it may be reused once the call's work on the stream has finished.  Results
  * repeat bit for bit: no sum depends on the order in which workgroups run.
  * Offsets are 64 bits wide.

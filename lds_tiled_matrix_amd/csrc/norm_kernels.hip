@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/linear/xpose_linear.h"
 #include "linear_device.h"
 #include "linear_kernels.h"
@@ -239,11 +241,15 @@ hipError_t launch_norm(const NormArgs &a, hipStream_t s) {
   const void *kernel = reinterpret_cast<const void *>(&norm_kernel<T, OUT, TR, NC>);
   // as many workgroups as run at once: a few more would run after all others
   // (16384 x 4096 bfloat16 takes 45 us, 51 with 6 of which 5 fit)
-  static const int at_once = [&] {
-    int n = 0;
-    return hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, norm_threads(TR), 0) == hipSuccess && n > 0 ? n : 1;
-  }();
-  const int64_t grid = (a.rows + per - 1) / per, most = 256 * (int64_t)at_once;
+  static std::atomic<int> at_once{0};  // of a compute unit; kept once it is known
+  int n = at_once.load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, norm_threads(TR), 0) == hipSuccess && n > 0)
+      at_once.store(n, std::memory_order_relaxed);
+    else
+      n = 1;
+  }
+  const int64_t grid = (a.rows + per - 1) / per, most = 256 * (int64_t)n;
   return launch(kernel, a, dim3((uint32_t)(grid < most ? grid : most)), norm_threads(TR), s);
 }
 template <typename T, Out OUT>
