@@ -329,6 +329,9 @@ const Tensor &tensor_of(PyObject *o, const char *what) {
   return THPVariable_Unpack(o);
 }
 
+// Whether a gradient's elements fill one stretch of memory, in any order.
+bool is_dense(const Tensor &t) { return t.is_non_overlapping_and_dense(); }
+
 // (norm, out): `out` is the caller's own sequence, or a new list.
 py::tuple clip_grad_norm(const py::object &given_grads, double max_norm, double eps, const py::object &given_out,
                          const py::object &stream) {
@@ -354,7 +357,7 @@ py::tuple clip_grad_norm(const py::object &given_grads, double max_norm, double 
     const Tensor &g = tensor_of(PySequence_Fast_GET_ITEM(grads.ptr(), i), "grads");
     same_device(first, g);
     const int code = dtype_code(g.scalar_type(), "grads");
-    if (!g.is_non_overlapping_and_dense()) bad_value("a gradient does not fill one stretch of memory");
+    if (!is_dense(g)) bad_value("a gradient does not fill one stretch of memory");
     if (make) PyList_SET_ITEM(out.ptr(), i, THPVariable_Wrap(at::empty_like(g)));
     const Tensor &o = tensor_of(PySequence_Fast_GET_ITEM(out.ptr(), i), "out");
     if (!make && !o.is_same(g)) {
@@ -378,8 +381,6 @@ py::tuple clip_grad_norm(const py::object &given_grads, double max_norm, double 
   on.returns(norm);
   return py::make_tuple(norm, make ? out : given_out);
 }
-
-bool is_dense(const Tensor &t) { return t.is_non_overlapping_and_dense(); }
 
 }  // namespace
 
