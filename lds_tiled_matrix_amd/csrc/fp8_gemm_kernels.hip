@@ -209,12 +209,12 @@ __device__ inline void reads_and_barrier() {
 // miss the L2 cache held up every block).
 //
 // What bounds it: at 256 x 256 a block of k reads 192 KiB of LDS and writes 64,
-// which at 128 bytes a cycle are the 2,048 cycles of its products, so both run
-// full; 8192^3 takes 410 to 420 us with powers of two (2.6 PFLOP/s, the clock
-// down to 1.9 GHz), 480 to 490 with tile scales and 530 to 550 with row scales,
+// which at 128 bytes a cycle are the 2,048 cycles of its products, so both are
+// near full; 8192^3 takes 410 to 420 us with powers of two (2.6 PFLOP/s, the clock
+// down to 1.7 to 2.0 GHz), 480 to 490 with tile scales and 530 to 550 with row scales,
 // whose multiply-adds take turns with the products.  The exact kernels (128 x 128, two
 // workgroups on a compute unit) spend as many cycles on widening and scaling as
-// on products: 4096^3 takes 130 us (1.06 PFLOP/s).
+// on products: 4096^3 takes 130 to 137 us (1.0 PFLOP/s).
 //
 // b's rows of one operand: lane l has row 32 (j / 2) + 8 (l / 4) + 4 (j % 2) +
 // l % 4 of the wave's 64, so that over two j a lane's results are 8 neighbours
@@ -507,8 +507,8 @@ hipError_t launch_tile(const Fp8GemmArgs &a, Fp8GemmMode mode, hipStream_t s) {
 // Serving: reading b bounds it.  A workgroup has 16 rows of b and up to 16 MS
 // of a; its waves take the blocks of k in turn, straight from memory into the
 // instruction's registers, two or four at a time, and their sums are added through
-// LDS in the waves' order.  One token through 4096 x 4096 takes 5.9 us (2.8 TB/s;
-// the launch is over half of it), through 4096 x 8192 8 us.  A long k and few
+// LDS in the waves' order.  One token through 4096 x 4096 takes 6.0 us (2.8 TB/s;
+// the launch is over half of it), through 4096 x 8192 9 to 10 us.  A long k and few
 // rows of b go in slices, as for the tiles.
 constexpr int kSkinnyWaves = 8;
 

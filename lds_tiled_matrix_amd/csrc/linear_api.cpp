@@ -96,11 +96,14 @@ struct GemmPlan {
 
 constexpr int64_t kMaxSplits = 16;
 
-// Estimated microseconds of a product on MI355X, for choosing among kernels.
-// Fitted to 160 shapes from 1 x 64 x 128 to 5000 x 4096 x 8192, with bfloat16
-// and with float32 results, each timed with every kernel and 1 to 16 slices:
-// the choice is within 12% of the fastest for all but one of them, which takes
-// 17% more.
+// Estimated microseconds of a product on MI355X, for choosing among kernels,
+// fitted to timings of products with m up to 500 and n up to 4096.  Of 435 shapes
+// from 1 x 64 x 128 to 4352 x 28672 x 8192 (128 x 128 scales of b), each timed
+// with every kernel, with eight counts of slices from 1 to 16 and as chosen here,
+// the choice is within 12% of the fastest for 417 with bfloat16 results and 424
+// with float32 ones.  The worst at n <= 4096 takes 16% (float32 25%) more.  Past
+// that, where nothing was fitted, a few rows may take half as much again:
+// 1 x 14336 x 2048 takes 15.9 us in 16 slices as chosen, 10.5 in 4.
 //
 // Tiles: a start, then a block of k takes `one` while the compute units hold a
 // workgroup each and `two` with two of the 128 x 128 tiles on each (of 256 x

@@ -98,9 +98,10 @@ constexpr int norm_threads(int tr) { return tr <= 64 ? 256 : tr; }
 // Workgroups stay: a group of TR lanes walks over rows `groups` apart with the
 // weight and bias in registers (read anew for each row they are four times a
 // bfloat16 row's bytes: 8192 x 8192 took 56 us so), and the next row's loads
-// are under way while this one is worked on: 45 us, 6.0 TB/s.  Rows of odd
-// lengths: 12345 x 6789 bfloat16 84 us; 107 with loads of single elements at a
-// row's end, which cannot stay under way.
+// are under way while this one is worked on: 43 us, 6.2 TB/s (the kernel's own
+// time; a call among others 44 to 50).  Rows of odd lengths: 12345 x 6789 bfloat16
+// 79 us; with loads of single elements at a row's end, which cannot stay under
+// way, a quarter more.
 template <typename T, Out OUT, int TR, int NC>
 __global__ __launch_bounds__(norm_threads(TR)) void norm_kernel(NormArgs a) {
   __shared__ float lds[2][TR > 64 ? TR / 64 : 1];
@@ -263,7 +264,8 @@ hipError_t norm(const NormArgs &a, hipStream_t s) {
   // Where twice the lanes would be little more than half used, three chunks a
   // lane, if rows fill the card so (five waves a SIMD): 4000 x 9000 bfloat16 30
   // us, 42 on 1024 lanes; 16384 x 2800 to e4m3 42 and 51; but 64 x 4519 5.7 and
-  // 4.8.  float32 to float32 is bound by memory either way.
+  // 4.8.  float32 to float32 is near what memory allows without (8192 x 8192 97
+  // us, of which a copy would take 85).
   if constexpr (sizeof(T) == 2 || OUT != kTensor) {
     const auto three = [&](int64_t lanes) {
       return a.cols > 2 * 8 * lanes && a.cols <= 3 * 8 * lanes && a.rows * lanes >= 256 * 1280;
@@ -298,8 +300,8 @@ hipError_t norm(const NormArgs &a, int dtype, hipStream_t s) {
 // them up column by column, all in a fixed order.  8192 x 4096 bfloat16 takes
 // 44 us (4.6 TB/s; memory bounds it at 32).  Two rows' loads under way instead of
 // one gain nothing.
-// Short rows: 100000 x 128 bfloat16 takes 22 us, 76 with a wave a row and a sum
-// a wave; 4096 x 1024 11.8 us, 16.6 with a sum a wave.
+// Short rows: 100000 x 128 bfloat16 takes 20 us, 75 with a wave a row and a sum
+// a wave; 4096 x 1024 12 us, 17 with a sum a wave.
 
 template <typename T, int TR, int NC>
 __global__ __launch_bounds__(norm_threads(TR)) void norm_bwd_kernel(NormBwdArgs a) {
