@@ -20,7 +20,11 @@ stream, nothing else.
 The operators of a normalised linear layer in 8-bit floating point
 (``include/linear/xpose_linear.h``: ``fp8_gemm``, ``fp8_quantize``,
 ``layer_norm``, ``layer_norm_quantize``, ``layer_norm_backward`` and
-``clip_grad_norm``) are in ``linear.py`` and are names of this package too.
+``clip_grad_norm``) are in ``linear.py`` and are names of this package too, as
+are those of what stands around such a layer in a residual stream
+(``include/linear/xpose_block.h``: ``rms_norm``, ``rms_norm_quantize``,
+``rms_norm_backward``, ``adapters``, ``adapters_backward`` and ``dropout``),
+which are in ``block.py``.
 """
 from __future__ import annotations
 
@@ -513,3 +517,6 @@ from .linear import (  # noqa: E402  (needs the names above)
     LINEAR_EXPORTS, LINEAR_POW2, XposeClipTensor, XposeFp8GemmInfo,
     clip_grad_norm, fp8_gemm, fp8_gemm_plan, fp8_quantize, layer_norm,
     layer_norm_backward, layer_norm_quantize)
+from .block import (  # noqa: E402
+    BLOCK_EXPORTS, adapters, adapters_backward, dropout, rms_norm,
+    rms_norm_backward, rms_norm_quantize)

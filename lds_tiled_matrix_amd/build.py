@@ -1,5 +1,6 @@
 """Build libxpose.so for gfx950 in-tree, and _linear.so, the torch side of
-linear.py, which is host code and built where a torch with HIP is installed.
+linear.py and block.py, which is host code and built where a torch with HIP is
+installed.
 
     python lds_tiled_matrix_amd/build.py
 
@@ -17,11 +18,12 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libxpose.so")
-TORCH_SOURCE = "linear_torch.cpp"
+TORCH_SOURCES = ["linear_torch.cpp", "block_torch.cpp"]
 TORCH_LIB = os.path.join(HERE, "_linear.so")
 SOURCES = ["xpose_kernels.hip", "xpose_api.cpp", "sgemm_kernels.hip",
            "sgemm_api.cpp", "fp8_gemm_kernels.hip", "quantize_kernels.hip",
-           "norm_kernels.hip", "linear_api.cpp"]
+           "norm_kernels.hip", "linear_api.cpp", "rms_norm_kernels.hip",
+           "adapter_kernels.hip", "block_api.cpp"]
 ARCH = "gfx950"
 
 
@@ -90,7 +92,7 @@ def build_torch(verbose: bool = False) -> str | None:
            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(rocm, "include"),
            "-isystem", sysconfig.get_paths()["include"],
-           os.path.join(CSRC, TORCH_SOURCE), "-o", tmp,
+           *(os.path.join(CSRC, src) for src in TORCH_SOURCES), "-o", tmp,
            "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python",
            "-ltorch_cpu", "-lc10", "-lc10_hip",
            "-L" + HERE, "-l:libxpose.so", "-Wl,-rpath,$ORIGIN"]
