@@ -100,9 +100,10 @@ int xpose_adapters(int64_t m, int64_t n, int64_t k, int64_t rank,
                    int64_t ld_base, void *out, int64_t ld_out,
                    int32_t out_dtype, float *hidden, void *workspace,
                    int64_t workspace_bytes, void *stream);
-/* The workspace, 16-byte aligned, of a call with or without `hidden`. */
+/* The workspace, 16-byte aligned, of a call with x of x_size bytes an element
+ * (1: e4m3, 2 or 4), with or without `hidden`. */
 int xpose_adapters_workspace(int64_t m, int64_t k, int64_t rank, int64_t count,
-                             int32_t hidden, int64_t *bytes);
+                             int32_t x_size, int32_t hidden, int64_t *bytes);
 
 /* The gradients for dout, that of out; with dh[i] = alpha scale[l] dout[i] B[l]:
  *

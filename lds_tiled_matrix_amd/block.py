@@ -35,7 +35,7 @@ def _signatures():
         "xpose_rms_norm_backward": [i64, i64, p, i64, p, i64, i32, p, p, i64, p, i32, p, i64, p, p, i64, p],
         "xpose_rms_norm_backward_workspace": [i64, i64, i64_p],
         "xpose_adapters": sizes + [p, i64, p, i64] + weights + [p, i64, p, i64, i32, p, p, i64, p],
-        "xpose_adapters_workspace": [i64, i64, i64, i64, i32, i64_p],
+        "xpose_adapters_workspace": [i64, i64, i64, i64, i32, i32, i64_p],
         "xpose_adapters_backward": sizes + [p, i64, p, i64] + weights + [p, p, i64, p, i64, i32, p, p, p, i64, p],
         "xpose_adapters_backward_workspace": [i64, i64, i64, i64, i64, i32, i64_p],
         "xpose_dropout": [i64, i64, p, i64, i32, f64, u64, p, u64, p, i64, p, i64, p],

@@ -24,6 +24,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "../../include/linear/xpose_block.h"
 #include "block_kernels.h"
@@ -51,6 +52,69 @@ __device__ inline Vec8<T> guarded8(const T *row, int64_t len, int64_t col) {
   Vec8<T> v = load_row8(row, len, col);
   settle8<T>(v, len, col);
   return v;
+}
+
+// Chunks of 16 bytes: V of them from `col` on of a row of `len` elements.  As
+// with load_row8, what lies beyond the row's end is loaded from before it, and
+// settled into zeros later.
+template <typename E> constexpr int kChunk = 16 / (int)sizeof(E);
+typedef u32x4 u32x4_by2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_by4 __attribute__((aligned(4)));
+// 16 bytes of elements E as they lie in memory; e4m3 rows have them aligned
+template <typename E>
+using Chunk = typename std::conditional<sizeof(E) == 1, u32x4,
+                                        typename std::conditional<sizeof(E) == 2, u32x4_by2, u32x4_by4>::type>::type;
+// Rows shorter than one (SHORT) are read by elements: a kernel of its own, as
+// that path's waits would be in the way of the other one's loads.
+template <bool SHORT, typename E>
+__device__ inline u32x4 load_chunk(const E *row, int64_t len, int64_t col) {
+  constexpr int V = kChunk<E>;
+  if constexpr (!SHORT) return *reinterpret_cast<const Chunk<E> *>(row + (col < len - V ? col : len - V));
+  E v[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) v[e] = col + e < len ? row[col + e] : (E)0.f;
+  u32x4 w;
+  __builtin_memcpy(&w, v, 16);
+  return w;
+}
+template <typename E>
+__device__ inline void settle_chunk(u32x4 &v, int64_t len, int64_t col) {
+  constexpr int V = kChunk<E>;
+  if (len < V || col <= len - V) return;
+  const int64_t past = col + V - len;
+  const int by = past < V ? (int)past : V, words = by * (int)sizeof(E) / 4;
+  uint32_t w[5] = {v[0], v[1], v[2], v[3], 0};
+#pragma unroll
+  for (int d = 4; d; d /= 2)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (words & d) w[i] = i + d < 4 ? w[i + d] : 0;
+  if constexpr (sizeof(E) == 2)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (by & 1) w[i] = w[i] >> 16 | w[i + 1] << 16;
+  v = u32x4{w[0], w[1], w[2], w[3]};
+}
+template <typename E>
+__device__ inline void store_chunk(E *row, int64_t len, int64_t col, const float (&f)[kChunk<E>]) {
+  constexpr int V = kChunk<E>;
+  typedef E any __attribute__((ext_vector_type(V), aligned(sizeof(E))));
+  if (col + V <= len) {
+    any r;
+#pragma unroll
+    for (int e = 0; e < V; ++e) r[e] = (E)f[e];
+    *reinterpret_cast<any *>(row + col) = r;
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (col + e < len) row[col + e] = (E)f[e];
+  }
+}
+template <typename E> __device__ inline float chunk_at(const u32x4 &v, int e) {
+  if constexpr (sizeof(E) == 4) return __uint_as_float(v[e]);
+  E r[8];
+  __builtin_memcpy(r, &v, 16);
+  return (float)r[e];
 }
 
 // sum[i][j] += sum over the lanes' eight values of w[i] x[j]: lane l has row
@@ -93,13 +157,17 @@ __device__ inline Vec8<T> widen8(uint32_t lo, uint32_t hi) {
   return r;
 }
 
-// The adapter of row t0 + lane in the lanes below ROWS, -1 for none and -2 for no row.
-template <int ROWS>
-__device__ inline int tile_ids(const int32_t *ids, int64_t m, int count, int64_t t0, int lane) {
-  const int64_t row = t0 + lane;
-  if (lane >= ROWS || row >= m) return -2;
-  const int id = ids[row];
-  return (uint32_t)id < (uint32_t)count ? id : -1;
+// What is the same in all lanes, in a scalar register: a quotient is not by itself.
+__device__ inline int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// The adapter of row t0 + lane in the lanes below `rows`, -1 for none and -2 for
+// no row; the number itself is loaded before it is asked for.
+__device__ inline int raw_id(const int32_t *ids, int64_t m, int64_t t0, int lane) {
+  return ids[min(t0 + lane, m - 1)];
+}
+__device__ inline int tile_id(int raw, int64_t m, int count, int64_t t0, int rows, int lane) {
+  if (lane >= rows || t0 + lane >= m) return -2;
+  return (uint32_t)raw < (uint32_t)count ? raw : -1;
 }
 
 // f(adapter, lanes whose rows have it) for every adapter of a tile that falls
@@ -119,36 +187,178 @@ __device__ __forceinline__ void each_adapter(int id, int slot, int slots, F &&f)
 //
 // h = x w^T: the rows of w (the rank) are the instruction's first operand, the
 // rows of x its second, so a lane's results are four ranks of one row.  The
-// four waves of a workgroup share out its columns in blocks of 128 and add
-// their sums up at the end; a lane takes chunks of 8 columns at 64 (s / 2) + 16
-// (l / 16) + 8 (s % 2), which in e4m3 are 16 bytes for two of them.
-constexpr int kShrinkWaves = 4, kShrinkThreads = 64 * kShrinkWaves;
+// waves of a workgroup share out the columns in steps of 128 bytes of x and add
+// their sums up at the end.
+//
+// The instruction wants another row in each of 16 neighbouring lanes.  Loaded
+// so, every lane is a memory request of its own, and a compute unit gets 16
+// bytes a cycle (measured 36 GB/s, from the caches too; 4001 x 4096 bfloat16
+// took 18 us).  So 8 lanes load 128 bytes of a row (100 to 120 GB/s), two steps
+// ahead, and the step goes through the wave's own piece of LDS: no barriers.  A
+// row's 8 chunks there are permuted by an exclusive or with bits 1 to 3 of the
+// row, which spreads the reads of 16 rows over all banks.  Weights that come with
+// the rank along their rows (WT, B in the backward pass) are turned around by
+// the reads.
+template <typename T, bool Q> using ShrinkX = typename std::conditional<Q, uint8_t, T>::type;
+constexpr int kShrinkWaves = 8, kShrinkThreads = 64 * kShrinkWaves;
 
-template <typename T, bool Q, int NI, int NR>
+__device__ inline int swizzle(int row) { return (row >> 1) & 7; }
+
+// Steps whose loads are under way together, as registers allow.
+template <typename T, bool Q, int NI, int NR> constexpr int shrink_depth() {
+  return NI + NR * (Q ? (int)sizeof(T) : 1) <= 3 ? 4 : 2;
+}
+
+// A step of 128 bytes of x's rows and R times as many of w's, as loaded.
+template <bool Q, int NI, int NW> struct ShrinkStep {
+  u32x4 x[NI][2], w[NW][2];
+  float scale[Q ? NI : 1];
+};
+
+// Four halves of a column of LDS: lane l of 16 gets those at place l of the
+// four rows of 16 that lanes 4 j and on address, 8 bytes each.
+__device__ inline u32x2 turn4(const uint8_t *p) {
+  typedef short i16x4 __attribute__((ext_vector_type(4)));
+  auto *lds = (__attribute__((address_space(3))) uint8_t *)p;
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                       (__attribute__((address_space(3))) i16x4 *)lds));
+}
+
+// The rows of adapter l, in order, behind those of all adapters before it, which
+// are counted for that here too: ids are read by each adapter's workgroup, from
+// the caches.  A wave has a stretch of rows, 512 of them under way.
+__device__ inline void adapter_rows(const ShrinkArgs &a, int l, int32_t *lds) {
+  constexpr int WAVES = kShrinkWaves;
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const int64_t stretch = (a.m + 64 * WAVES - 1) / (64 * WAVES) * 64;
+  const int64_t begin = wave * stretch, end = min(begin + stretch, a.m);
+  auto ids8 = [&](int64_t i0, int (&id)[8]) {  // -1 past the end
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const int64_t i = i0 + 64 * s + lane;
+      id[s] = i < end ? a.ids[i] : -1;
+    }
+  };
+  int before = 0, mine = 0;
+  for (int64_t i0 = begin; i0 < end; i0 += 512) {
+    int id[8];
+    ids8(i0, id);
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      before += (uint32_t)id[s] < (uint32_t)l;
+      mine += id[s] == l;
+    }
+  }
+#pragma unroll
+  for (int d = 32; d; d /= 2) {
+    before += __shfl_xor(before, d);
+    mine += __shfl_xor(mine, d);
+  }
+  if (lane == 0) {
+    lds[wave] = before;
+    lds[WAVES + wave] = mine;
+  }
+  __syncthreads();
+  int at = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) at += lds[w];
+  if (tid == 0) a.starts[l] = at;
+  int place = at;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    if (w < wave) place += lds[WAVES + w];
+    at += lds[WAVES + w];
+  }
+  for (int64_t i0 = begin; i0 < end; i0 += 512) {
+    int id[8];
+    ids8(i0, id);
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const uint64_t all = __ballot(id[s] == l);
+      if (id[s] == l) a.order[place + __popcll(all & ((1ull << lane) - 1))] = (int32_t)(i0 + 64 * s + lane);
+      place += __popcll(all);
+    }
+  }
+  if (tid == 0 && l == a.count - 1) a.starts[a.count] = at;
+}
+
+template <typename T, bool Q, int NI, int NR, bool WT, bool SHORT>
 __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(ShrinkArgs a) {
-  constexpr int ROWS = 16 * NI;
-  __shared__ f32x4 lds[kShrinkWaves][NI * NR][64];
+  using XT = ShrinkX<T, Q>;
+  constexpr int WAVES = kShrinkWaves, THREADS = kShrinkThreads, DEPTH = shrink_depth<T, Q, NI, NR>();
+  constexpr int ROWS = 16 * NI, R = Q ? (int)sizeof(T) : 1, NW = NR * R, UNITS = NI + NW;
+  constexpr int kStep = 128 / (int)sizeof(XT);  // columns
+  using Step = ShrinkStep<Q, NI, NW>;
+  static_assert(UNITS * 2 >= NI * NR);  // the sums fit where the steps were
+  __shared__ __align__(16) uint8_t lds[WAVES][UNITS * 2048];
   const int tid = threadIdx.x, lane = tid % 64, i16 = lane % 16, g = lane / 16;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
+  uint8_t *const mine = lds[wave];
+  if (blockIdx.x >= a.tiles) {
+    if (blockIdx.y == 0 && blockIdx.z == 0) adapter_rows(a, (int)(blockIdx.x - a.tiles), (int32_t *)lds[0]);
+    return;
+  }
   const int64_t t0 = (int64_t)blockIdx.x * ROWS;
-  const int slice = blockIdx.y / a.slots, slot = blockIdx.y % a.slots;
+  const int slice = scalar(blockIdx.y / a.slots), slot = scalar(blockIdx.y % a.slots);
   const int r0 = blockIdx.z * 16 * NR;
-  const int id = tile_ids<ROWS>(a.ids, a.m, a.count, t0, lane);
+  const int id = tile_id(raw_id(a.ids, a.m, t0, lane), a.m, a.count, t0, ROWS, lane);
   float *h = a.h + slice * a.slice;
+  const int steps = (int)((a.k + kStep - 1) / kStep), whole = (int)(a.k / kStep);
+  const int first = scalar(slice * a.steps_per_slice);
+  const int last = scalar(min(first + a.steps_per_slice, steps)), last_whole = scalar(min(last, whole));
+  // what this lane loads: rows lane / 8 and 8 more, and their chunk
+  const int row_in[2] = {lane / 8, lane / 8 + 8};
+  const int chunk[2] = {lane % 8 ^ swizzle(row_in[0]), lane % 8 ^ swizzle(row_in[1])};
+  const XT *x[NI][2];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+      x[i][o] = (const XT *)a.x + min(t0 + 16 * i + row_in[o], a.m - 1) * a.ldx + chunk[o] * kChunk<XT>;
+
+  // WT: w's rows are its columns, 16 ranks of each are a row of a unit in LDS,
+  // and this lane loads a chunk of ranks of one of the step's columns.
+  auto turned_column = [&](int o) { return (64 * o + lane) / (int)sizeof(T); };
+  auto turned_rank = [&](int o) { return (64 * o + lane) % (int)sizeof(T) * kChunk<T>; };
+
+  auto load_x = [&](int step, Step &v, auto ragged) {
+    constexpr bool RAGGED = decltype(ragged)::value;
+    const int64_t c0 = (int64_t)step * kStep;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      if constexpr (Q) v.scale[i] = a.scale_x[c0 / kStep * a.ld_scale_x + min(t0 + 16 * i + i16, a.m - 1)];
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        if constexpr (!RAGGED) {
+          v.x[i][o] = *reinterpret_cast<const Chunk<XT> *>(x[i][o] + c0);
+        } else if constexpr (Q) {  // the 16 bytes that hold a row's end are all there
+          const int64_t left = a.k - c0 - chunk[o] * 16;
+          v.x[i][o] = *reinterpret_cast<const u32x4 *>(x[i][o] + (left > 0 ? c0 : -chunk[o] * 16));
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int64_t in = left - 4 * b;
+            v.x[i][o][b] &= in >= 4 ? ~0u : in <= 0 ? 0u : (1u << (8 * (int)in)) - 1;
+          }
+        } else {
+          const int64_t at = chunk[o] * kChunk<XT>;
+          if (a.k < kChunk<XT>) {
+            v.x[i][o] = load_chunk<true>(x[i][o] - at, a.k, c0 + at);
+          } else {
+            v.x[i][o] = load_chunk<false>(x[i][o] - at, a.k, c0 + at);
+            settle_chunk<XT>(v.x[i][o], a.k, c0 + at);
+          }
+        }
+      }
+    }
+  };
   if (slot == 0) {
-    uint64_t none = __ballot(id == -1);
+    const uint64_t none = __ballot(id == -1);
     if (none)
-      for (int i = tid; i < ROWS * 16 * NR; i += kShrinkThreads) {
+      for (int i = tid; i < ROWS * 16 * NR; i += THREADS) {
         const int row = i / (16 * NR), r = r0 + i % (16 * NR);
         if ((none >> row & 1) && r < a.rank) h[(t0 + row) * a.rank + r] = 0.f;
       }
   }
-  const int64_t blocks = (a.k + kBlock - 1) / kBlock, whole = a.k / kBlock;
-  const int64_t first = (int64_t)slice * a.blocks_per_slice;
-  const int64_t last = min(first + a.blocks_per_slice, blocks);
-  int64_t row[NI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) row[i] = min(t0 + 16 * i + i16, a.m - 1);
 
   each_adapter(id, slot, a.slots, [&](int d, uint64_t match) {
     f32x4 sum[NI][NR];
@@ -157,98 +367,198 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(ShrinkArgs a) {
 #pragma unroll
       for (int q = 0; q < NR; ++q) sum[i][q] = f32x4{0.f, 0.f, 0.f, 0.f};
     const T *w0 = (const T *)a.w + d * a.stride_w;
-    const T *w[NR];
+    const T *w[NR][2];
 #pragma unroll
-    for (int q = 0; q < NR; ++q) w[q] = w0 + min(r0 + 16 * q + i16, a.rank - 1) * a.ldw;
+    for (int q = 0; q < NR; ++q)
+#pragma unroll
+      for (int o = 0; o < 2; ++o)
+        w[q][o] = WT ? w0 + turned_column(o) * a.ldw
+                     : w0 + min(r0 + 16 * q + row_in[o], a.rank - 1) * a.ldw + chunk[o] * kChunk<T>;
 
-    auto block = [&](int64_t kb, auto ragged) {
+    auto load_w = [&](int step, Step &v, auto ragged) {
       constexpr bool RAGGED = decltype(ragged)::value;
-      const int64_t c0 = kb * kBlock + 16 * g;
-      Vec8<T> wv[NR][4];
-      auto load_w = [&](int s) {
-        const int64_t c = c0 + 64 * (s / 2) + 8 * (s % 2);
+      const int64_t c0 = (int64_t)step * kStep;
 #pragma unroll
-        for (int q = 0; q < NR; ++q) {
-          if constexpr (RAGGED) wv[q][s] = guarded8(w[q], a.k, c);
-          else wv[q][s] = load_raw8(w[q] + c, 8);
-        }
-      };
-      if constexpr (Q) {
-        u32x4 xq[NI][2];
-        float scale[NI];
+      for (int q = 0; q < NR; ++q)
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const uint8_t *x = (const uint8_t *)a.x + row[i] * a.ldx;
-          scale[i] = a.scale_x[kb * a.ld_scale_x + row[i]];
+        for (int j = 0; j < R; ++j)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int64_t col = c0 + 64 * c;
-            if constexpr (RAGGED) {  // the 16 bytes that hold a row's end are all there
-              const int64_t left = a.k - col;
-              xq[i][c] = *reinterpret_cast<const u32x4 *>(x + (left > 0 ? col : 0));
-#pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                const int64_t in = left - 4 * b;
-                xq[i][c][b] &= in >= 4 ? ~0u : in <= 0 ? 0u : (1u << (8 * (int)in)) - 1;
-              }
+          for (int o = 0; o < 2; ++o) {
+            u32x4 &to = v.w[q * R + j][o];
+            if constexpr (WT) {
+              const int64_t past = RAGGED ? max(c0 + turned_column(o) - (a.k - 1), (int64_t)0) : 0;  // the last column again
+              to = load_chunk<SHORT>(w[q][o] + (c0 - past) * a.ldw, a.rank, r0 + 16 * q + turned_rank(o));
+              if (RAGGED && past) to = u32x4{0, 0, 0, 0};
             } else {
-              xq[i][c] = *reinterpret_cast<const u32x4 *>(x + col);
+              const int64_t c = c0 + 8 * j * kChunk<T>;
+              if constexpr (!RAGGED) {
+                to = *reinterpret_cast<const Chunk<T> *>(w[q][o] + c);
+              } else {
+                const int64_t at = chunk[o] * kChunk<T>;
+                if (a.k < kChunk<T>) {
+                  to = load_chunk<true>(w[q][o] - at, a.k, c + at);
+                } else {
+                  to = load_chunk<false>(w[q][o] - at, a.k, c + at);
+                  settle_chunk<T>(to, a.k, c + at);
+                }
+              }
+            }
+          }
+    };
+    // chunk c of row i16 of a unit
+    auto read = [&](int unit, int c) {
+      return *reinterpret_cast<const u32x4 *>(mine + unit * 2048 + i16 * 128 + (c ^ swizzle(i16)) * 16);
+    };
+    // eight values along the columns, chunks g + 4 b and (float32) g + 4 b + 4 of x, of rank 16 q + i16
+    auto read_w = [&](int q, int b) {
+      Vec8<T> to;
+      constexpr int C = (int)sizeof(Vec8<T>) / 16;
+      if constexpr (!WT) {
+        u32x4 c[C];
+#pragma unroll
+        for (int j = 0; j < C; ++j) c[j] = read(NI + q, g + 4 * (b * C + j));
+        __builtin_memcpy(&to, c, sizeof to);
+      } else if constexpr (C == 1) {
+        u32x2 c[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          c[h] = turn4(mine + (NI + q) * 2048 + ((g + 4 * b) * 8 + 4 * h + i16 / 4) * 32 + i16 % 4 * 8);
+        __builtin_memcpy(&to, c, sizeof to);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          to.v[e / 4][e % 4] = *reinterpret_cast<const float *>(mine + (NI + q) * 2048 + ((g + e / 4 * 4) * 4 + e % 4) * 64 + i16 * 4);
+      }
+      return to;
+    };
+    auto multiply = [&](Step &v) {
+      if constexpr (WT && !SHORT)
+#pragma unroll
+        for (int q = 0; q < NR; ++q)
+#pragma unroll
+          for (int o = 0; o < 2; ++o) settle_chunk<T>(v.w[q][o], a.rank, r0 + 16 * q + turned_rank(o));
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) *reinterpret_cast<u32x4 *>(mine + i * 2048 + o * 1024 + lane * 16) = v.x[i][o];
+#pragma unroll
+        for (int j = 0; j < NW; ++j)
+          *reinterpret_cast<u32x4 *>(mine + (NI + j) * 2048 + o * 1024 + lane * 16) = v.w[j][o];
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if constexpr (Q) {
+        f32x4 part[NI][NR];
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int q = 0; q < NR; ++q) part[i][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {  // chunks g and g + 4 of x: 16 values
+          u32x4 xc[NI];
+#pragma unroll
+          for (int i = 0; i < NI; ++i) xc[i] = read(i, g + 4 * b);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            Vec8<T> xv[NI];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) xv[i] = widen8<T>(xc[i][2 * half], xc[i][2 * half + 1]);
+#pragma unroll
+            for (int q = 0; q < NR; ++q) {
+              Vec8<T> wv;
+              u32x4 wc[R / 2];
+#pragma unroll
+              for (int j = 0; j < R / 2; ++j) {
+                const int c = (g + 4 * b) * R + half * (R / 2) + j;  // of w's row
+                wc[j] = read(NI + q * R + c / 8, c % 8);
+              }
+              __builtin_memcpy(&wv, wc, sizeof wv);
+#pragma unroll
+              for (int i = 0; i < NI; ++i) part[i][q] = multiply8<T>(wv, xv[i], part[i][q]);
             }
           }
         }
 #pragma unroll
-        for (int s = 0; s < 4; ++s) load_w(s);
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          f32x4 part[NR];
-#pragma unroll
-          for (int q = 0; q < NR; ++q) part[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const Vec8<T> x = widen8<T>(xq[i][s / 2][s % 2 * 2], xq[i][s / 2][s % 2 * 2 + 1]);
-#pragma unroll
-            for (int q = 0; q < NR; ++q) part[q] = multiply8<T>(wv[q][s], x, part[q]);
-          }
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
           for (int q = 0; q < NR; ++q)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum[i][q][e] = __builtin_fmaf(part[q][e], scale[i], sum[i][q][e]);
-        }
+            for (int e = 0; e < 4; ++e) sum[i][q][e] = __builtin_fmaf(part[i][q][e], v.scale[i], sum[i][q][e]);
       } else {
-        Vec8<T> xv[NI][4];
+        constexpr int C = (int)sizeof(Vec8<T>) / 16;  // chunks of eight values
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int64_t c = c0 + 64 * (s / 2) + 8 * (s % 2);
+        for (int b = 0; b < 2 / C; ++b) {
+          Vec8<T> xv[NI], wv[NR];
+          auto get = [&](int unit, Vec8<T> &to) {
+            u32x4 c[C];
 #pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            const T *x = (const T *)a.x + row[i] * a.ldx;
-            if constexpr (RAGGED) xv[i][s] = guarded8(x, a.k, c);
-            else xv[i][s] = load_raw8(x + c, 8);
-          }
-          load_w(s);
-        }
+            for (int j = 0; j < C; ++j) c[j] = read(unit, g + 4 * (b * C + j));
+            __builtin_memcpy(&to, c, sizeof to);
+          };
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+          for (int i = 0; i < NI; ++i) get(i, xv[i]);
+#pragma unroll
+          for (int q = 0; q < NR; ++q) wv[q] = read_w(q, b);
 #pragma unroll
           for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int q = 0; q < NR; ++q) sum[i][q] = multiply8<T>(wv[q][s], xv[i][s], sum[i][q]);
+            for (int q = 0; q < NR; ++q) sum[i][q] = multiply8<T>(wv[q], xv[i], sum[i][q]);
+        }
       }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
-    int64_t kb = first + wave;
-    for (; kb < min(last, whole); kb += kShrinkWaves) block(kb, std::false_type{});
-    if (kb < last) block(kb, std::true_type{});
+    // Where paths meet that have other loads under way, or in another order, all
+    // of them are waited for: so one way through the main loop, no conditions in
+    // it, and the last steps behind it.
+    const int start = first + wave;
+    if (start < last_whole) {
+      Step v[DEPTH];
+      auto fetch = [&](int step, Step &to) {
+        load_x(step, to, std::false_type{});
+        load_w(step, to, std::false_type{});
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      int step = start;
+      if (start + (2 * DEPTH - 1) * WAVES < last_whole) {
+#pragma unroll
+        for (int u = 0; u < DEPTH; ++u) fetch(start + u * WAVES, v[u]);
+        for (; step + (2 * DEPTH - 1) * WAVES < last_whole; step += DEPTH * WAVES)
+#pragma unroll
+          for (int u = 0; u < DEPTH; ++u) {
+            multiply(v[u]);
+            fetch(step + (DEPTH + u) * WAVES, v[u]);
+          }
+      } else {
+#pragma unroll
+        for (int u = 0; u < DEPTH; ++u)
+          if (start + u * WAVES < last_whole) fetch(start + u * WAVES, v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < DEPTH; ++u) {
+        if (step + u * WAVES < last_whole) multiply(v[u]);
+        if (step + (DEPTH + u) * WAVES < last_whole) fetch(step + (DEPTH + u) * WAVES, v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < DEPTH - 1; ++u)
+        if (step + (DEPTH + u) * WAVES < last_whole) multiply(v[u]);
+    }
+    if (whole < last && wave == (whole - first) % WAVES) {
+      Step end;
+      load_x(whole, end, std::true_type{});
+      load_w(whole, end, std::true_type{});
+      multiply(end);
+    }
 
+    f32x4 *sums = reinterpret_cast<f32x4 *>(mine);
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int q = 0; q < NR; ++q) lds[wave][i * NR + q][lane] = sum[i][q];
+      for (int q = 0; q < NR; ++q) sums[(i * NR + q) * 64 + lane] = sum[i][q];
     __syncthreads();
     const float factor = a.scaled ? a.alpha * (a.scale ? a.scale[d] : 1.f) : 1.f;
-    for (int f = wave; f < NI * NR; f += kShrinkWaves) {
-      f32x4 v = lds[0][f][lane];
+    for (int f = wave; f < NI * NR; f += WAVES) {
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int o = 1; o < kShrinkWaves; ++o) v += lds[o][f][lane];
+      for (int o = 0; o < WAVES; ++o) v += reinterpret_cast<const f32x4 *>(lds[o])[f * 64 + lane];
       const int in = f / NR * 16 + i16, r = r0 + f % NR * 16 + 4 * g;
       if (!(match >> in & 1)) continue;
       float *to = h + (t0 + in) * a.rank + r;
@@ -261,32 +571,29 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(ShrinkArgs a) {
           if (r + e < a.rank) to[e] = v[e];
       }
     }
-    __syncthreads();  // before the next adapter's sums
+    __syncthreads();  // before the next adapter's steps
   });
-}
-
-constexpr int kSlicesThreads = 256;
-__global__ __launch_bounds__(kSlicesThreads) void slices_kernel(SlicesArgs a) {
-  for (int64_t i = (int64_t)blockIdx.x * kSlicesThreads + threadIdx.x; i < a.count;
-       i += (int64_t)gridDim.x * kSlicesThreads) {
-    float s = a.in[i];
-    for (int p = 1; p < a.slices; ++p) s += a.in[p * a.count + i];
-    a.out[i] = s;
-  }
 }
 
 // ----- expand ------------------------------------------------------------------------
 //
-// out = base + h w^T, the rows of w (columns of out) as the first operand: a
-// lane's results lie in one row of out.  Which of the 32 columns of two
-// instructions is which of their rows is chosen so that a lane has eight
-// neighbours of them, and four lanes 32.
+// out = base + h w^T, the rows of h as the first operand and the rows of w
+// (columns of out) as the second: a lane has four rows of one column.  Which of
+// the columns of eight instructions is which of their rows is chosen so that a
+// lane has 16 bytes of each of its rows, and 16 lanes 256: with a row a lane
+// instead, as in `shrink` above, 4001 x 8192 bfloat16 took 41 us.
+//
+// A workgroup has WR waves of 16 rows under each other and 4 / WR side by side,
+// 128 columns each, and goes down the rows, the next tile's ids, base and h on
+// their way.  Its columns of w lie in LDS as operands, 32 ranks at a time, until
+// another adapter's are needed.
 //
 // h is float32 and stays it: for 16-bit weights it goes to the matrix cores as
 // the sum of three bfloat16 numbers (24 bits; they have float32's range, which
 // float16 has not), float16 weights as the sum of two.  Next to reading base
 // and writing out, the products are free.
-constexpr int kExpandThreads = 256, kExpandCols = 256;  // of a workgroup; 64 a wave
+constexpr int kExpandWaves = 4, kExpandThreads = 64 * kExpandWaves;
+constexpr int kExpandCols = 128;  // of a wave
 
 // Eight float32 numbers as operands of multiply_split.
 template <typename T> struct Split8 {
@@ -317,7 +624,7 @@ template <typename T> __device__ inline f32x4 multiply_split(const Vec8<T> &w, c
 template <>
 __device__ inline f32x4 multiply_split<__bf16>(const Vec8<__bf16> &w, const Split8<__bf16> &h, f32x4 sum) {
 #pragma unroll
-  for (int p = 2; p >= 0; --p) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16((bf16x8)w.v, h.part[p], sum, 0, 0, 0);
+  for (int p = 2; p >= 0; --p) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h.part[p], (bf16x8)w.v, sum, 0, 0, 0);
   return sum;
 }
 template <>
@@ -330,168 +637,190 @@ __device__ inline f32x4 multiply_split<_Float16>(const Vec8<_Float16> &w, const 
     lo[e] = (__bf16)(__builtin_fabsf(f) < __builtin_inff() ? f - (float)hi[e] : 0.f);
   }
 #pragma unroll
-  for (int p = 1; p >= 0; --p) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, h.part[p], sum, 0, 0, 0);
+  for (int p = 1; p >= 0; --p) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h.part[p], lo, sum, 0, 0, 0);
 #pragma unroll
-  for (int p = 2; p >= 0; --p) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, h.part[p], sum, 0, 0, 0);
+  for (int p = 2; p >= 0; --p) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h.part[p], hi, sum, 0, 0, 0);
   return sum;
 }
 template <> __device__ inline f32x4 multiply_split<float>(const Vec8<float> &w, const Split8<float> &h, f32x4 sum) {
 #pragma unroll
   for (int e = 0; e < 8; ++e)
-    sum = __builtin_amdgcn_mfma_f32_16x16x4f32(w.v[e / 4][e % 4], h.v[e], sum, 0, 0, 0);
+    sum = __builtin_amdgcn_mfma_f32_16x16x4f32(h.v[e], w.v[e / 4][e % 4], sum, 0, 0, 0);
   return sum;
 }
 
-template <typename T, typename O, int NI>
+template <typename T, typename O, int WR, bool WT, bool SHORT>
 __global__ __launch_bounds__(kExpandThreads) void expand_kernel(ExpandArgs a) {
-  constexpr int ROWS = 16 * NI;
+  constexpr int V = kChunk<O>, P = 8 / V, ROWS = 16 * WR, COLS = kExpandCols * kExpandWaves / WR;
+  // An operand's 64 lanes follow each other, 16 bytes each (float32: twice), a
+  // bank group on from the previous operand's.
+  constexpr int C = (int)sizeof(Vec8<T>) / 16, kOperand = 1024 * C + 16;
+  __shared__ __align__(16) uint8_t lds[COLS / 16 * kOperand];
   const int tid = threadIdx.x, lane = tid % 64, i16 = lane % 16, g = lane / 16;
-  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
-  const int64_t col_tiles = (a.n + kExpandCols - 1) / kExpandCols;
-  const int slot = blockIdx.x % a.slots;
-  const int64_t tile = blockIdx.x / a.slots;
-  const int64_t t0 = tile / col_tiles * ROWS, n0 = tile % col_tiles * kExpandCols + wave * 64;
-  const int id = tile_ids<ROWS>(a.ids, a.m, a.count, t0, lane);
-  if (n0 >= a.n) return;
+  const int wave = scalar(tid / 64);
+  const int slot = scalar(blockIdx.x % a.slots), place = scalar(blockIdx.x / a.slots);
+  const int first = scalar(place / a.strips) * a.tiles, last = scalar(min(first + a.tiles, (int)((a.m + ROWS - 1) / ROWS)));
+  const int64_t n0 = (int64_t)scalar(place % a.strips) * COLS;
+  const int side = wave / WR;      // of the waves side by side
+  const int in0 = wave % WR * 16;  // this wave's rows of a tile
+  auto column = [&](int p) { return n0 + side * kExpandCols + 16 * V * p + V * i16; };  // the first of V
+  const bool has_columns = n0 + side * kExpandCols < a.n;
 
-  // the 64 columns of this wave, those rows of `match`
-  auto store = [&](uint64_t match, const f32x4 (&sum)[NI][4], bool add) {
+  struct Tile {
+    int id;
+    u32x4 base[4][P];
+    Vec8<float> h;  // of the first 32 ranks, of all slices
+  };
+  auto load_h = [&](int64_t row0, int c) {
+    const float *h = a.h + min(row0 + i16, a.m - 1) * a.rank;
+    const int r = c + 8 * g;
+    auto slice = [&](int s) {
+      if constexpr (SHORT) return load_raw8(h + s * a.slice + r, valid8(a.rank - r));
+      else return load_row8(h + s * a.slice, a.rank, r);
+    };
+    Vec8<float> f = slice(0);
+    if (a.slices > 1) {
+      Vec8<float> more[3];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      if (!(match >> (16 * i + i16) & 1)) continue;
-      const int64_t row = t0 + 16 * i + i16;
+      for (int s = 0; s < 3; ++s) more[s] = slice(min(s + 1, a.slices - 1));
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int64_t col = n0 + 32 * p + 8 * g;
-        const int valid = valid8(a.n - col);
-        float f[8] = {};
-        if (a.base) load8((const O *)a.base + row * a.ld_base + col, valid, f);
+      for (int s = 0; s < 3; ++s)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (add) f[e] += sum[i][2 * p + e / 4][e % 4];
-        store8((O *)a.out + row * a.ld_out + col, valid, f);
-      }
+        for (int e = 0; e < 8; ++e) f.v[e / 4][e % 4] += s + 1 < a.slices ? more[s].v[e / 4][e % 4] : 0.f;
     }
+    return f;
+  };
+  // without conditions, so that the loads stay together: what is out of the
+  // tile, or no base, is read from elsewhere and not used
+  const O *base = (const O *)(a.base ? a.base : a.out);
+  const int64_t ld_base = a.base ? a.ld_base : a.ld_out;
+  auto load = [&](int tile, Tile &to) {
+    const int64_t t0 = (int64_t)tile * ROWS, row0 = t0 + in0;
+    to.id = raw_id(a.ids, a.m, t0, lane);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        to.base[e][p] = load_chunk<SHORT>(base + min(row0 + 4 * g + e, a.m - 1) * ld_base, a.n, column(p));
+    if (a.count) to.h = load_h(row0, 0);
   };
 
-  if (slot == 0 && a.base != a.out) {  // rows without an adapter
-    const uint64_t none = __ballot(id == -1);
-    f32x4 zero[NI][4];
-    if (none) store(none, zero, false);
-  }
-  each_adapter(id, slot, a.slots, [&](int d, uint64_t match) {
-    const T *w0 = (const T *)a.w + d * a.stride_w;
-    const float factor = a.alpha * (a.scale ? a.scale[d] : 1.f);
-    f32x4 sum[NI][4];
+  Tile now;
+  int has = -1;  // the adapter whose operands are in LDS
+  load(first, now);
+  // Here, where the adapter has to be waited for anyway: else the first tile's
+  // loads count as under way in all turns, and each waits for the next tile's.
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  for (int tile = first; tile < last; ++tile) {
+    const int64_t t0 = (int64_t)tile * ROWS, row0 = t0 + in0;
+    const bool here = has_columns && row0 < a.m;
+    const int id = tile_id(now.id, a.m, a.count, t0, ROWS, lane);
+    Tile next;
+    if (tile + 1 < last) load(tile + 1, next);
+    auto store = [&](uint64_t match, const f32x4 (&sum)[8], auto add) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+      for (int e = 0; e < 4; ++e) {
+        if (!(match >> (in0 + 4 * g + e) & 1)) continue;
+        O *to = (O *)a.out + (row0 + 4 * g + e) * a.ld_out;
 #pragma unroll
-      for (int p = 0; p < 4; ++p) sum[i][p] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int c = 0; c < a.rank; c += 32) {
-      const int r = c + 8 * g, valid = valid8(a.rank - r);
-      Vec8<T> w[4];
+        for (int p = 0; p < P; ++p) {
+          float y[V];
+          u32x4 b = now.base[e][p];
+          if constexpr (!SHORT) settle_chunk<O>(b, a.n, column(p));
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const int64_t col = n0 + 32 * (p / 2) + 8 * (i16 / 4) + 4 * (p % 2) + i16 % 4;
-        w[p] = load_raw8(w0 + min(col, a.n - 1) * a.ldw + r, valid);
+          for (int j = 0; j < V; ++j) {
+            y[j] = a.base ? chunk_at<O>(b, j) : 0.f;
+            if constexpr (decltype(add)::value) y[j] += sum[p * V + j][e];
+          }
+          store_chunk(to, a.n, column(p), y);
+        }
       }
+    };
+    if (slot == 0 && a.base != a.out && here) {
+      const uint64_t none = __ballot(id == -1);
+      const f32x4 nothing[8] = {};
+      if (none >> in0 & 0xffff) store(none, nothing, std::false_type{});
+    }
+    each_adapter(id, slot, a.slots, [&](int d, uint64_t match) {
+      const bool mine = here && (match >> in0 & 0xffff) != 0;
+      const float factor = a.alpha * (a.scale ? a.scale[d] : 1.f);
+      const T *w0 = (const T *)a.w + d * a.stride_w;
+      f32x4 sum[8];
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const float *h = a.h + min(t0 + 16 * i + i16, a.m - 1) * a.rank + r;
+      for (int j = 0; j < 8; ++j) sum[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int c = 0; c < a.rank; c += 32) {
+        if (a.rank > 32 || has != d) {
+          constexpr int EACH = COLS * 4 / kExpandThreads;  // chunks of eight, of 32 ranks of each column
+          Vec8<T> w[EACH];
+          if constexpr (!WT) {
+#pragma unroll
+            for (int u = 0; u < EACH; ++u) {
+              const int i = u * kExpandThreads + tid, r = c + i % 4 * 8;
+              const T *from = w0 + min(n0 + i / 4, a.n - 1) * a.ldw;
+              if constexpr (SHORT) w[u] = load_raw8(from + r, valid8(a.rank - r));
+              else w[u] = load_row8(from, a.rank, r);
+            }
+          } else {
+#pragma unroll
+            for (int u = 0; u < EACH; ++u) {
+              const int i = u * kExpandThreads + tid;
+              const int64_t col = n0 + i % (COLS / 8) * 8;
+              const T *from = w0 + min(c + i / (COLS / 8), a.rank - 1) * a.ldw;
+              if constexpr (SHORT) w[u] = load_raw8(from + col, valid8(a.n - col));
+              else w[u] = load_row8(from, a.n, col);
+            }
+          }
+          __syncthreads();  // the operands before these are done with
+#pragma unroll
+          for (int u = 0; u < EACH; ++u) {
+            const int i = u * kExpandThreads + tid;
+            auto operand = [&](int col) {  // and its lane of ranks 0 to 7
+              return lds + (col / kExpandCols * 8 + col % kExpandCols / (16 * V) * V + col % V) * kOperand + col / V % 16 * 16;
+            };
+            if constexpr (!WT) {
+              if constexpr (!SHORT) settle8<T>(w[u], a.rank, c + i % 4 * 8);
+              u32x4 v[C];
+              __builtin_memcpy(v, &w[u], sizeof v);
+              uint8_t *to = operand(i / 4) + i % 4 * 256;
+#pragma unroll
+              for (int q = 0; q < C; ++q) *reinterpret_cast<u32x4 *>(to + 1024 * q) = v[q];
+            } else {
+              const int col = i % (COLS / 8) * 8, r = i / (COLS / 8);
+              if constexpr (!SHORT) settle8<T>(w[u], a.n, n0 + col);
+              T v[8];
+              __builtin_memcpy(v, &w[u], sizeof v);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                uint8_t *to = operand(col + e) + r / 8 * 256 + r % 8 * (int)sizeof(T) / 16 * 1024 + r % 8 * (int)sizeof(T) % 16;
+                *reinterpret_cast<T *>(to) = c + r < a.rank ? v[e] : (T)0.f;
+              }
+            }
+          }
+          __syncthreads();
+          has = d;
+        }
+        if (!mine) continue;
+        Vec8<float> raw = c == 0 ? now.h : load_h(row0, c);
+        if constexpr (!SHORT) settle8<float>(raw, a.rank, c + 8 * g);
         float f[8];
-        load8(h, valid, f);
-        for (int s = 1; s < a.slices; ++s) {
-          float more[8];
-          load8(h + s * a.slice, valid, more);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] += more[e];
+        for (int e = 0; e < 8; ++e) f[e] = at8<float>(raw, e) * factor;
+        Split8<T> h;
+        h.set(f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint8_t *p = lds + (side * 8 + j) * kOperand + lane * 16;
+          u32x4 v[C];
+#pragma unroll
+          for (int q = 0; q < C; ++q) v[q] = *reinterpret_cast<const u32x4 *>(p + 1024 * q);
+          Vec8<T> wj;
+          __builtin_memcpy(&wj, v, sizeof v);
+          sum[j] = multiply_split<T>(wj, h, sum[j]);
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= factor;
-        Split8<T> hs;
-        hs.set(f);
-#pragma unroll
-        for (int p = 0; p < 4; ++p) sum[i][p] = multiply_split<T>(w[p], hs, sum[i][p]);
       }
-    }
-    store(match, sum, true);
-  });
-}
-
-// ----- what the backward pass lays out first -------------------------------------------
-//
-// One launch: the first `count` workgroups find an adapter's rows each, all
-// others transpose 256 columns (of A) or rows (of B) of an adapter's weights.
-// An adapter's rows follow those of all adapters before it, so its workgroup
-// counts those too; ids are read by each of them, from the caches.
-constexpr int kPrepThreads = 256, kPrepRanks = 32;
-
-template <typename T>
-__global__ __launch_bounds__(kPrepThreads) void adapter_prep_kernel(AdapterPrepArgs a) {
-  __shared__ T tile[kPrepThreads][kPrepRanks + 1];
-  __shared__ int32_t waves[2][kPrepThreads / 64];
-  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
-  int64_t block = blockIdx.x;
-  if (a.order) {
-    if (block < a.count) {
-      const int l = (int)block;
-      int before = 0;
-      for (int64_t i = tid; i < a.m; i += kPrepThreads) before += (uint32_t)a.ids[i] < (uint32_t)l;
-#pragma unroll
-      for (int d = 32; d; d /= 2) before += __shfl_xor(before, d);
-      if (lane == 0) waves[0][wave] = before;
-      __syncthreads();
-      int at = 0;
-#pragma unroll
-      for (int w = 0; w < kPrepThreads / 64; ++w) at += waves[0][w];
-      if (tid == 0) a.starts[l] = at;
-      for (int64_t i0 = 0; i0 < a.m; i0 += kPrepThreads) {
-        const int64_t i = i0 + tid;
-        const bool mine = i < a.m && a.ids[i] == l;
-        const uint64_t in_wave = __ballot(mine);
-        __syncthreads();
-        if (lane == 0) waves[1][wave] = __popcll(in_wave);
-        __syncthreads();
-        int place = at + __popcll(in_wave & ((1ull << lane) - 1));
-#pragma unroll
-        for (int w = 0; w < kPrepThreads / 64; ++w) {
-          if (w < wave) place += waves[1][w];
-          at += waves[1][w];
-        }
-        if (mine) a.order[place] = (int32_t)i;
-      }
-      if (tid == 0 && l == a.count - 1) a.starts[a.count] = at;
-      return;
-    }
-    block -= a.count;
-  }
-  const int64_t tiles_a = a.at ? (a.k + kPrepThreads - 1) / kPrepThreads * a.count : 0;
-  const bool of_b = block >= tiles_a;
-  if (of_b) block -= tiles_a;
-  const int64_t len = of_b ? a.n : a.k, tiles = (len + kPrepThreads - 1) / kPrepThreads;
-  const int64_t l = block / tiles, c0 = block % tiles * kPrepThreads;
-  const int cols = (int)min(len - c0, (int64_t)kPrepThreads);
-  for (int r0 = 0; r0 < a.rank; r0 += kPrepRanks) {
-    const int ranks = min(a.rank - r0, kPrepRanks);
-    __syncthreads();
-    if (of_b) {
-      const T *b = (const T *)a.b + l * a.stride_b + c0 * a.ldb + r0;
-      for (int i = tid; i < cols * ranks; i += kPrepThreads) tile[i / ranks][i % ranks] = b[i / ranks * a.ldb + i % ranks];
-    } else {
-      const T *w = (const T *)a.a + l * a.stride_a + (int64_t)r0 * a.lda + c0;
-      if (tid < cols)
-        for (int r = 0; r < ranks; ++r) tile[tid][r] = w[r * a.lda + tid];
-    }
-    __syncthreads();
-    if (of_b) {
-      T *to = (T *)a.bt + (l * a.rank + r0) * a.n + c0;
-      if (tid < cols)
-        for (int r = 0; r < ranks; ++r) to[r * a.n + tid] = tile[tid][r];
-    } else {
-      T *to = (T *)a.at + (l * a.k + c0) * a.rank + r0;
-      for (int i = tid; i < cols * ranks; i += kPrepThreads)
-        to[(int64_t)(i / ranks) * a.rank + i % ranks] = tile[i / ranks][i % ranks];
-    }
+      if (mine) store(match, sum, std::true_type{});
+    });
+    now = next;
   }
 }
 
@@ -502,7 +831,7 @@ __global__ __launch_bounds__(kPrepThreads) void adapter_prep_kernel(AdapterPrepA
 // as a lane has one rank or eight neighbouring columns of one row in four.
 //
 // An adapter's rows are cut into pieces, a workgroup for 128 columns of each.
-// An adapter of one piece is done with that; the pieces of larger ones go to
+// An adapter of one piece, or none, is done with that; the pieces of larger ones go to
 // the workspace and a second launch adds them up, in their order.  Adapter l's
 // pieces are the numbers starts[l] / piece + l and on: there are enough
 // numbers between one adapter's first and the next one's.  Workspace slots,
@@ -511,27 +840,37 @@ constexpr int kGradThreads = 256, kGradCols = 128, kGradWaves = 4;
 
 __device__ inline int grad_pieces(int rows, int piece) { return (rows + piece - 1) / piece; }
 
-template <typename T, int NR>
-__global__ __launch_bounds__(kGradThreads) void adapter_grad_kernel(AdapterGradArgs a, int64_t tiles_k, int64_t tiles) {
+template <typename T, int NR> struct GradRows {
+  Vec8<T> v[4];
+  float u[4][NR];
+};
+
+template <typename T, int NR, bool SHORT>
+__global__ __launch_bounds__(kGradThreads) void adapter_grad_kernel(AdapterGradArgs a, int tiles_k, int tiles) {
+  constexpr int DEPTH = NR * (int)sizeof(T) <= 4 ? 3 : 2;  // blocks of rows under way, as registers allow
   __shared__ f32x4 lds[NR][8][64];
   const int tid = threadIdx.x, lane = tid % 64, i16 = lane % 16, g = lane / 16;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
-  const int64_t number = blockIdx.x / tiles, tile = blockIdx.x % tiles;
+  const int number = scalar((int)(blockIdx.x / (uint32_t)tiles)), tile = scalar((int)(blockIdx.x % (uint32_t)tiles));
   const int r0 = blockIdx.y * 16 * NR;
-  int lo = 0, hi = a.count - 1;  // the last adapter whose first number is no later
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (a.starts[mid] / a.piece + mid <= number) lo = mid; else hi = mid - 1;
+  // the last adapter whose first number is no later, by 64 of them at a time
+  int l = 0;
+  for (int left = a.count; left > 1;) {
+    const int step = (left + 63) / 64, probe = lane * step;
+    const bool no_later = probe < left && a.starts[l + probe] / a.piece + l + probe <= number;
+    const int p = __popcll(__ballot(no_later)) - 1;  // the first one's is 0
+    l += p * step;
+    left = min(step, left - p * step);
   }
-  const int l = __builtin_amdgcn_readfirstlane(lo);
-  const int start = a.starts[l], rows = a.starts[l + 1] - start;
-  const int j = (int)(number - (start / a.piece + l));
+  l = scalar(l);
+  const int start = scalar(a.starts[l]), rows = scalar(a.starts[l + 1]) - start;
+  const int j = number - (start / a.piece + l);
   const int pieces = grad_pieces(rows, a.piece);
-  if (j >= pieces) return;
+  if (j >= max(pieces, 1)) return;  // the first one of an adapter of no rows stores zeros
   const int begin = start + j * a.piece, end = min(begin + a.piece, start + rows);
 
   const bool of_b = tile >= tiles_k;
-  const int64_t cols = of_b ? a.n : a.k, c0 = (of_b ? tile - tiles_k : tile) * kGradCols;
+  const int64_t cols = of_b ? a.n : a.k, c0 = (of_b ? tile - tiles_k : tile) * (int64_t)kGradCols;
   const T *v = (const T *)(of_b ? a.dout : a.x);
   const int64_t ldv = of_b ? a.lddout : a.ldx;
   const float *u = of_b ? a.h : a.dh;
@@ -543,29 +882,60 @@ __global__ __launch_bounds__(kGradThreads) void adapter_grad_kernel(AdapterGradA
   for (int q = 0; q < NR; ++q)
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[q][e] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int p0 = begin + 16 * wave; p0 < end; p0 += 16 * kGradWaves) {
+  // 16 rows at a time, the next ones' loads under way and the numbers of those
+  // after them; past the end the last row is read, for nothing
+  GradRows<T, NR> rows_of[DEPTH];
+  int numbers[DEPTH];
+  auto number_of = [&](int p0) { return a.order[min(p0 + i16, end - 1)]; };
+  // rows with these numbers; then numbers are those of p0
+  auto load = [&](int &numbers, int p0, GradRows<T, NR> &to) {
+    int64_t row[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) row[s] = __shfl(numbers, 4 * s + g);
+    __builtin_amdgcn_sched_barrier(0);
+    numbers = number_of(p0);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const int at = p0 + 4 * s + g;
-      const bool in = at < end;
-      const int64_t row = a.order[in ? at : end - 1];
-      const Vec8<T> vv = cols < 8 ? load_raw8(v + row * ldv + col, valid8(cols - col)) : load_row8(v + row * ldv, cols, col);
-      float uu[NR];
+      const T *from = v + row[s] * ldv;
+      if constexpr (SHORT) to.v[s] = load_raw8(from + col, valid8(cols - col));
+      else to.v[s] = load_row8(from, cols, col);
 #pragma unroll
-      for (int q = 0; q < NR; ++q) {
-        const int r = r0 + 16 * q + i16;
-        uu[q] = u[row * a.rank + min(r, a.rank - 1)];
-        if (!in) uu[q] = 0.f;
-      }
-      Vec8<T> settled = vv;
-      if (cols >= 8) settle8<T>(settled, cols, col);
+      for (int q = 0; q < NR; ++q) to.u[s][q] = u[row[s] * a.rank + min(r0 + 16 * q + i16, a.rank - 1)];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // `whole`: all 16 rows are this piece's; else those past it may hold anything
+  auto multiply = [&](int p0, GradRows<T, NR> &rows, auto whole) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const bool in = decltype(whole)::value || p0 + 4 * s + g < end;
+      if constexpr (!SHORT) settle8<T>(rows.v[s], cols, col);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float f = in ? at8<T>(settled, e) : 0.f;
+        const float f = in ? at8<T>(rows.v[s], e) : 0.f;
 #pragma unroll
-        for (int q = 0; q < NR; ++q) sum[q][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(uu[q], f, sum[q][e], 0, 0, 0);
+        for (int q = 0; q < NR; ++q)
+          sum[q][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(in ? rows.u[s][q] : 0.f, f, sum[q][e], 0, 0, 0);
       }
     }
+  };
+  // as in shrink_kernel, one way through the loop
+  constexpr int kApart = 16 * kGradWaves;
+  const int start_at = begin + 16 * wave;
+  if (start_at < end) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) numbers[d] = number_of(start_at + d * kApart);
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) load(numbers[d], start_at + (DEPTH + d) * kApart, rows_of[d]);
+    for (int p0 = start_at; p0 < end; p0 += DEPTH * kApart)
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) {
+        const int at = p0 + d * kApart;
+        if (at + 16 <= end) multiply(at, rows_of[d], std::true_type{});
+        else if (at < end) multiply(at, rows_of[d], std::false_type{});
+        load(numbers[d], at + 2 * DEPTH * kApart, rows_of[d]);
+      }
   }
   // the waves' sums, one after the other
   for (int w = 0; w < kGradWaves; ++w) {
@@ -584,7 +954,7 @@ __global__ __launch_bounds__(kGradThreads) void adapter_grad_kernel(AdapterGradA
   };
   const int ranks = min(a.rank - r0, 16 * NR), here = (int)min(cols - c0, (int64_t)kGradCols);
   const int64_t slot = 2 * (int64_t)(start / a.piece) + j, each = (int64_t)a.rank * (a.k + a.n);
-  const bool done = pieces == 1;
+  const bool done = pieces <= 1;
   if (of_b) {
     float *to = done ? a.db + (int64_t)l * a.n * a.rank : a.partial + slot * each + (int64_t)a.rank * a.k;
     for (int i = tid; i < ranks * here; i += kGradThreads)
@@ -598,11 +968,11 @@ __global__ __launch_bounds__(kGradThreads) void adapter_grad_kernel(AdapterGradA
   }
 }
 
-// Adapters of no rows get zeros, those of several pieces their sum.
+// Adapters of several pieces get their sum.
 __global__ __launch_bounds__(kGradThreads) void adapter_grad_sum_kernel(AdapterGradArgs a, int64_t groups) {
   const int l = (int)(blockIdx.x / groups);
   const int start = a.starts[l], pieces = grad_pieces(a.starts[l + 1] - start, a.piece);
-  if (pieces == 1) return;
+  if (pieces <= 1) return;
   const int64_t of_a = (int64_t)a.rank * a.k, each = of_a + (int64_t)a.rank * a.n;
   const float *p = a.partial + 2 * (int64_t)(start / a.piece) * each;
   for (int64_t i = (int64_t)(blockIdx.x % groups) * kGradThreads + threadIdx.x; i < each; i += groups * kGradThreads) {
@@ -610,6 +980,7 @@ __global__ __launch_bounds__(kGradThreads) void adapter_grad_sum_kernel(AdapterG
                          : (a.db ? a.db + l * (each - of_a) + (i - of_a) : nullptr);
     if (!to) continue;
     float s = 0.f;
+#pragma unroll 8
     for (int j = 0; j < pieces; ++j) s += p[j * each + i];
     *to = s;
   }
@@ -669,46 +1040,86 @@ hipError_t launch(const void *kernel, dim3 grid, int threads, hipStream_t s, con
   return hipLaunchKernel(kernel, grid, dim3(threads), args, 0, s);
 }
 
-template <typename T, bool Q, int NI>
-hipError_t shrink(const ShrinkArgs &a, dim3 grid, hipStream_t s) {
-  if (a.rank <= 16) {
-    return launch(reinterpret_cast<const void *>(&shrink_kernel<T, Q, NI, 1>), grid, kShrinkThreads, s, a);
-  }
-  if (a.rank <= 32) return launch(reinterpret_cast<const void *>(&shrink_kernel<T, Q, NI, 2>), grid, kShrinkThreads, s, a);
-  grid.z = (uint32_t)((a.rank + 63) / 64);
-  return launch(reinterpret_cast<const void *>(&shrink_kernel<T, Q, NI, 4>), grid, kShrinkThreads, s, a);
-}
-template <typename T, bool Q>
+template <typename T, bool Q, int NI, int NR, bool WT, bool SHORT>
 hipError_t shrink(const ShrinkArgs &a, const ShrinkPlan &p, hipStream_t s) {
-  const int64_t rows = 16 * p.row_tiles;
-  const dim3 grid((uint32_t)((a.m + rows - 1) / rows), (uint32_t)(p.slices * p.slots));
-  return p.row_tiles == 1 ? shrink<T, Q, 1>(a, grid, s) : shrink<T, Q, 2>(a, grid, s);
+  const dim3 grid(a.tiles + (a.order ? (uint32_t)a.count : 0), (uint32_t)(p.slices * p.slots),
+                  (uint32_t)((a.rank + 16 * NR - 1) / (16 * NR)));
+  return launch(reinterpret_cast<const void *>(&shrink_kernel<T, Q, NI, NR, WT, SHORT>), grid, kShrinkThreads, s, a);
+}
+template <typename T, bool Q, int NI, bool WT>
+hipError_t shrink_rank(const ShrinkArgs &a, const ShrinkPlan &p, hipStream_t s) {
+  // weights take 16 registers a rank and step, twice that next to e4m3, four
+  // times in float32 next to e4m3: more would spill
+  constexpr int most = Q ? (sizeof(T) == 2 && NI == 1 ? 2 : 1) : sizeof(T) == 2 && NI == 1 && !WT ? 4 : 2;
+  if constexpr (WT)
+    if (a.rank < kChunk<T>) return shrink<T, Q, NI, 1, WT, true>(a, p, s);
+  if (a.rank <= 16 || most == 1) return shrink<T, Q, NI, 1, WT, false>(a, p, s);
+  return a.rank <= 32 || most == 2 ? shrink<T, Q, NI, most < 2 ? 1 : 2, WT, false>(a, p, s)
+                                   : shrink<T, Q, NI, most, WT, false>(a, p, s);
+}
+template <typename T, bool Q, bool WT>
+hipError_t shrink(ShrinkArgs a, const ShrinkPlan &p, hipStream_t s) {
+  constexpr int most = Q && sizeof(T) == 4 ? 1 : 2;
+  const int64_t rows = 16 * std::min(p.row_tiles, most);
+  a.tiles = a.h ? (uint32_t)((a.m + rows - 1) / rows) : 0;
+  return p.row_tiles == 1 ? shrink_rank<T, Q, 1, WT>(a, p, s) : shrink_rank<T, Q, most, WT>(a, p, s);
 }
 template <typename T>
 hipError_t shrink(const ShrinkArgs &a, const ShrinkPlan &p, hipStream_t s) {
-  return a.scale_x ? shrink<T, true>(a, p, s) : shrink<T, false>(a, p, s);
+  return a.turned ? shrink<T, false, true>(a, p, s) : a.scale_x ? shrink<T, true, false>(a, p, s) : shrink<T, false, false>(a, p, s);
 }
 
+template <typename T, typename O, int WR, bool WT, bool SHORT>
+hipError_t expand(ExpandArgs a, const ExpandPlan &p, hipStream_t s) {
+  const void *kernel = reinterpret_cast<const void *>(&expand_kernel<T, O, WR, WT, SHORT>);
+  // tiles of a workgroup: as many workgroups as run at once (4001 x 8192 bfloat16,
+  // two of a compute unit: 44 us with 8 tiles, 49 with 6, 54 with one)
+  static std::atomic<int> at_once{0};  // of a compute unit; kept once it is known
+  int n = at_once.load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kExpandThreads, 0) == hipSuccess && n > 0)
+      at_once.store(n, std::memory_order_relaxed);
+    else
+      n = 1;
+  }
+  const int64_t most = 256 * (int64_t)n, side = (int64_t)a.strips * a.slots;
+  const int64_t down = std::max<int64_t>(1, most / side);
+  a.tiles = (int32_t)((p.tiles + down - 1) / down);
+  const int64_t groups = (p.tiles + a.tiles - 1) / a.tiles * side;
+  return launch(kernel, dim3((uint32_t)groups), kExpandThreads, s, a);
+}
+template <typename T, typename O, bool WT, bool SHORT>
+hipError_t expand(const ExpandArgs &a, const ExpandPlan &p, hipStream_t s) {
+  return p.waves_down == 4 ? expand<T, O, 4, WT, SHORT>(a, p, s) : expand<T, O, 1, WT, SHORT>(a, p, s);
+}
+template <typename T, typename O, bool WT>
+hipError_t expand(const ExpandArgs &a, const ExpandPlan &p, hipStream_t s) {
+  // shorter than a load: of base, of h and w's ranks or columns
+  return a.n < 8 || a.rank < 8 ? expand<T, O, WT, true>(a, p, s) : expand<T, O, WT, false>(a, p, s);
+}
 template <typename T, typename O>
 hipError_t expand(const ExpandArgs &a, const ExpandPlan &p, hipStream_t s) {
-  const dim3 grid((uint32_t)p.workgroups);
-  return p.row_tiles == 1 ? launch(reinterpret_cast<const void *>(&expand_kernel<T, O, 1>), grid, kExpandThreads, s, a)
-                          : launch(reinterpret_cast<const void *>(&expand_kernel<T, O, 2>), grid, kExpandThreads, s, a);
+  return a.turned ? expand<T, O, true>(a, p, s) : expand<T, O, false>(a, p, s);
 }
 
+template <typename T, bool SHORT>
+const void *grad_kernel(int nr) {
+  return nr == 1   ? reinterpret_cast<const void *>(&adapter_grad_kernel<T, 1, SHORT>)
+         : nr == 2 ? reinterpret_cast<const void *>(&adapter_grad_kernel<T, 2, SHORT>)
+                   : reinterpret_cast<const void *>(&adapter_grad_kernel<T, 4, SHORT>);
+}
 template <typename T>
 hipError_t grad(const AdapterGradArgs &a, hipStream_t s) {
-  const int64_t tiles_k = a.da ? (a.k + kGradCols - 1) / kGradCols : 0;
-  const int64_t tiles = tiles_k + (a.db ? (a.n + kGradCols - 1) / kGradCols : 0);
+  const int tiles_k = a.da ? (int)((a.k + kGradCols - 1) / kGradCols) : 0;
+  const int tiles = tiles_k + (int)(a.db ? (a.n + kGradCols - 1) / kGradCols : 0);
   const int64_t numbers = a.m / a.piece + a.count;
   if (tiles == 0) return hipSuccess;
   const int nr = a.rank <= 16 ? 1 : a.rank <= 32 ? 2 : 4;
   const dim3 grid((uint32_t)(numbers * tiles), (uint32_t)((a.rank + 16 * nr - 1) / (16 * nr)));
-  const void *kernel = nr == 1   ? reinterpret_cast<const void *>(&adapter_grad_kernel<T, 1>)
-                       : nr == 2 ? reinterpret_cast<const void *>(&adapter_grad_kernel<T, 2>)
-                                 : reinterpret_cast<const void *>(&adapter_grad_kernel<T, 4>);
+  const bool narrow = (a.da && a.k < 8) || (a.db && a.n < 8);
+  const void *kernel = narrow ? grad_kernel<T, true>(nr) : grad_kernel<T, false>(nr);
   const hipError_t e = launch(kernel, grid, kGradThreads, s, a, tiles_k, tiles);
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || a.m <= a.piece) return e;  // no adapter has two pieces
   const int64_t values = (int64_t)a.rank * (a.k + a.n), most = 4096 / a.count + 1;
   const int64_t groups = std::min((values + kGradThreads - 1) / kGradThreads, most);
   return launch(reinterpret_cast<const void *>(&adapter_grad_sum_kernel), dim3((uint32_t)(groups * a.count)),
@@ -717,7 +1128,7 @@ hipError_t grad(const AdapterGradArgs &a, hipStream_t s) {
 
 }  // namespace
 
-ShrinkPlan shrink_plan(int64_t m, int64_t k, int64_t rank, int64_t count) {
+ShrinkPlan shrink_plan(int64_t m, int64_t k, int64_t rank, int64_t count, int x_size, bool whole) {
   ShrinkPlan p{};
   p.row_tiles = m <= 4096 ? 1 : 2;
   const int64_t tiles = (m + 16 * p.row_tiles - 1) / (16 * p.row_tiles);
@@ -725,31 +1136,27 @@ ShrinkPlan shrink_plan(int64_t m, int64_t k, int64_t rank, int64_t count) {
   const int64_t adapters = std::min<int64_t>(std::min<int64_t>(m, 16), count);
   p.slots = 1;
   while (p.slots < adapters && tiles * p.slots < 64) p.slots *= 2;
-  const int64_t blocks = std::max<int64_t>(1, (k + kBlock - 1) / kBlock);
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(16, 256 / (tiles * p.slots)));
-  const int64_t most = (blocks + kShrinkWaves - 1) / kShrinkWaves;  // a block for each wave
-  p.blocks_per_slice = (int)((blocks + std::min(want, most) - 1) / std::min(want, most));
-  p.slices = (int)((blocks + p.blocks_per_slice - 1) / p.blocks_per_slice);
+  const int64_t columns = 128 / x_size, steps = std::max<int64_t>(1, (k + columns - 1) / columns);
+  const int64_t room = whole ? 1 : std::max<int64_t>(1, 256 / (tiles * p.slots));
+  const int64_t slices = std::min(std::min<int64_t>(4, room), (steps + kShrinkWaves - 1) / kShrinkWaves);
+  p.steps_per_slice = (int)((steps + slices - 1) / slices);
+  p.slices = (int)((steps + p.steps_per_slice - 1) / p.steps_per_slice);
   return p;
 }
 hipError_t launch_shrink(const ShrinkArgs &a, const ShrinkPlan &p, int dtype, hipStream_t s) {
   return dtype == XPOSE_F32 ? shrink<float>(a, p, s) : dtype == XPOSE_F16 ? shrink<_Float16>(a, p, s) : shrink<__bf16>(a, p, s);
 }
 
-hipError_t launch_slices(const SlicesArgs &a, hipStream_t s) {
-  const int64_t groups = (a.count + kSlicesThreads - 1) / kSlicesThreads;
-  return launch(reinterpret_cast<const void *>(&slices_kernel), dim3((uint32_t)std::min<int64_t>(groups, 2048)),
-                kSlicesThreads, s, a);
-}
-
 ExpandPlan expand_plan(int64_t m, int64_t n, int64_t count) {
   ExpandPlan p{};
-  p.row_tiles = m <= 1024 ? 1 : 2;
-  const int64_t tiles = (m + 16 * p.row_tiles - 1) / (16 * p.row_tiles) * ((n + kExpandCols - 1) / kExpandCols);
-  const int64_t adapters = std::min<int64_t>(std::min<int64_t>(m, 16), count);
+  p.waves_down = m > 16 ? 4 : 1;
+  const int rows = 16 * p.waves_down, cols = kExpandCols * kExpandWaves / p.waves_down;
+  p.strips = (n + cols - 1) / cols;
+  p.tiles = (m + rows - 1) / rows;
+  // a tile's rows have so many adapters at most
+  const int64_t adapters = std::min(std::min(m, (int64_t)rows), count);
   p.slots = 1;
-  while (p.slots < adapters && tiles * p.slots < 512) p.slots *= 2;
-  p.workgroups = tiles * p.slots;
+  while (p.slots < adapters && p.tiles * p.strips * p.slots < 256) p.slots *= 2;
   return p;
 }
 hipError_t launch_expand(const ExpandArgs &a, const ExpandPlan &p, int dtype, int out_dtype, hipStream_t s) {
@@ -759,20 +1166,11 @@ hipError_t launch_expand(const ExpandArgs &a, const ExpandPlan &p, int dtype, in
   return out_dtype == XPOSE_F32 ? expand<__bf16, float>(a, p, s) : expand<__bf16, __bf16>(a, p, s);
 }
 
-hipError_t launch_adapter_prep(const AdapterPrepArgs &a, int dtype, hipStream_t s) {
-  auto tiles = [&](int64_t len) { return (len + kPrepThreads - 1) / kPrepThreads * a.count; };
-  const int64_t groups = (a.order ? a.count : 0) + (a.at ? tiles(a.k) : 0) + (a.bt ? tiles(a.n) : 0);
-  if (groups == 0) return hipSuccess;
-  const void *kernel = dtype == XPOSE_F32   ? reinterpret_cast<const void *>(&adapter_prep_kernel<float>)
-                       : dtype == XPOSE_F16 ? reinterpret_cast<const void *>(&adapter_prep_kernel<_Float16>)
-                                            : reinterpret_cast<const void *>(&adapter_prep_kernel<__bf16>);
-  return launch(kernel, dim3((uint32_t)groups), kPrepThreads, s, a);
-}
-
 int adapter_grad_piece(int64_t m, int64_t n, int64_t k) {
   const int64_t tiles = (n + kGradCols - 1) / kGradCols + (k + kGradCols - 1) / kGradCols;
-  int piece = 64;
-  while (piece < 4096 && m / piece * tiles > 1024) piece *= 2;
+  if (m <= 512) return 512;  // one piece an adapter: no second launch
+  int piece = 128;
+  while (piece < 4096 && m / piece * tiles > 768) piece *= 2;
   return piece;
 }
 int64_t adapter_grad_slots(int64_t m, int piece) { return m > piece ? 2 * (m / piece + 1) : 0; }

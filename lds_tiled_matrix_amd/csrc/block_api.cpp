@@ -182,15 +182,17 @@ static bool adapter_sizes(int64_t m, int64_t n, int64_t k, int64_t rank, int64_t
 }
 
 static bool expand_fits(int64_t m, int64_t n, int64_t count) {
-  return m == 0 || n == 0 || xpose::expand_plan(m, n, count).workgroups <= kMaxGroups;
+  if (m == 0 || n == 0) return true;
+  const xpose::ExpandPlan p = xpose::expand_plan(m, n, count);
+  return p.tiles * p.strips * p.slots <= kMaxGroups;
 }
 
-int xpose_adapters_workspace(int64_t m, int64_t k, int64_t rank, int64_t count, int32_t hidden, int64_t *bytes) {
-  if (!adapter_sizes(m, 0, k, rank, count) || !bytes) return XPOSE_EINVAL;
+int xpose_adapters_workspace(int64_t m, int64_t k, int64_t rank, int64_t count, int32_t x_size, int32_t hidden,
+                             int64_t *bytes) {
+  if (!adapter_sizes(m, 0, k, rank, count) || !bytes || (x_size != 1 && x_size != 2 && x_size != 4)) return XPOSE_EINVAL;
   Parts p;
   if (m && rank) {
-    const int slices = xpose::shrink_plan(m, k, rank, count).slices;
-    if (slices > 1 || !hidden) p.add(m * rank, slices, 4);
+    if (!hidden) p.add(m * rank, xpose::shrink_plan(m, k, rank, count, x_size, false).slices, 4);
   }
   *bytes = p.total();
   return XPOSE_OK;
@@ -204,12 +206,13 @@ int xpose_adapters(int64_t m, int64_t n, int64_t k, int64_t rank, int64_t count,
   if (!adapter_sizes(m, n, k, rank, count) || workspace_bytes < 0 || !expand_fits(m, n, count)) return XPOSE_EINVAL;
   const int size = size_of(dtype), out_size = size_of(out_dtype);
   if (!size || !out_size || (out_dtype != dtype && out_dtype != XPOSE_F32)) return XPOSE_EDTYPE;
+  const int x_size = scale_x ? 1 : size;
   int64_t need = 0;
-  int rc = xpose_adapters_workspace(m, k, rank, count, hidden != nullptr, &need);
+  int rc = xpose_adapters_workspace(m, k, rank, count, x_size, hidden != nullptr, &need);
   if (rc != XPOSE_OK) return rc;
   const bool some = m && rank && count;  // whether anything of A and x is read
   Ranges r;
-  r.matrix(x, some ? m : 0, k, ldx, scale_x ? 1 : size, scale_x ? 16 : size, false);
+  r.matrix(x, some ? m : 0, k, ldx, x_size, scale_x ? 16 : size, false);
   if (scale_x) r.matrix(scale_x, some ? ceil_div(k, kBlock) : 0, m, ld_scale_x, 4, 4, false);
   r.matrices(a, some ? count : 0, stride_a, rank, k, lda, size);
   r.matrices(b, some ? count : 0, stride_b, n, rank, ldb, size);
@@ -225,16 +228,16 @@ int xpose_adapters(int64_t m, int64_t n, int64_t k, int64_t rank, int64_t count,
   if (rc != XPOSE_OK || m == 0) return rc;
   if (!enough) return XPOSE_EWORKSPACE;
 
-  const float *h = hidden;
+  const float *h = hidden ? hidden : (const float *)workspace;
   int slices = 1;
   if (rank) {
-    const xpose::ShrinkPlan plan = xpose::shrink_plan(m, k, rank, count);
+    const xpose::ShrinkPlan plan = xpose::shrink_plan(m, k, rank, count, x_size, hidden != nullptr);
     xpose::ShrinkArgs s{};
     s.x = x;
     s.w = a;
     s.scale_x = scale_x;
     s.ids = ids;
-    s.h = need ? (float *)workspace : hidden;
+    s.h = hidden ? hidden : (float *)workspace;
     s.m = m;
     s.k = k;
     s.ldx = ldx;
@@ -244,17 +247,11 @@ int xpose_adapters(int64_t m, int64_t n, int64_t k, int64_t rank, int64_t count,
     s.slice = m * rank;
     s.rank = (int32_t)rank;
     s.count = (int32_t)count;
-    s.blocks_per_slice = plan.blocks_per_slice;
+    s.steps_per_slice = plan.steps_per_slice;
     s.slots = plan.slots;
     rc = hip(xpose::launch_shrink(s, plan, dtype, (hipStream_t)stream));
     if (rc != XPOSE_OK) return rc;
-    if (hidden && plan.slices > 1) {
-      rc = hip(xpose::launch_slices({(const float *)workspace, hidden, m * rank, plan.slices}, (hipStream_t)stream));
-      if (rc != XPOSE_OK) return rc;
-    } else if (!hidden) {
-      h = (const float *)workspace;
-      slices = plan.slices;
-    }
+    slices = plan.slices;
   }
   if (n == 0 || ((rank == 0 || count == 0) && base == out)) return XPOSE_OK;
   const int64_t used = rank ? count : 0;  // with no rank, no row has an adapter
@@ -277,6 +274,7 @@ int xpose_adapters(int64_t m, int64_t n, int64_t k, int64_t rank, int64_t count,
   e.rank = (int32_t)rank;
   e.count = (int32_t)used;
   e.slots = plan.slots;
+  e.strips = (int32_t)plan.strips;
   e.alpha = alpha;
   return hip(xpose::launch_expand(e, plan, dtype, out_dtype, (hipStream_t)stream));
 }
@@ -284,20 +282,17 @@ int xpose_adapters(int64_t m, int64_t n, int64_t k, int64_t rank, int64_t count,
 namespace {
 // Where the backward pass keeps what.
 struct BackwardParts {
-  int64_t at, bt, order, starts, dh, slices, partial, bytes;
+  int64_t order, starts, dh, partial, bytes;
   xpose::ShrinkPlan plan;
   int piece;
 };
 bool backward_parts(int64_t m, int64_t n, int64_t k, int64_t rank, int64_t count, int size, BackwardParts &w) {
   Parts p;
-  w.plan = xpose::shrink_plan(std::max<int64_t>(m, 1), n, rank, count);
+  w.plan = xpose::shrink_plan(std::max<int64_t>(m, 1), n, rank, count, size, true);
   w.piece = xpose::adapter_grad_piece(m, n, k);
-  w.at = p.add(count * rank, k, size);
-  w.bt = p.add(count * rank, n, size);
   w.order = p.add(m, 1, 4);
   w.starts = p.add(count + 1, 1, 4);
   w.dh = p.add(m * rank, 1, 4);
-  w.slices = p.add(w.plan.slices > 1 ? m * rank : 0, w.plan.slices, 4);
   w.partial = p.add(xpose::adapter_grad_slots(m, w.piece) * rank, k + n, 4);
   w.bytes = p.total();
   return p.fits();
@@ -327,8 +322,7 @@ int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank, int64
   if (!size || !dx_size || (dx_dtype != dtype && dx_dtype != XPOSE_F32)) return XPOSE_EDTYPE;
   BackwardParts w;
   if (!backward_parts(m, n, k, rank, count, size, w) ||
-      (m / w.piece + count) * (ceil_div(n, 128) + ceil_div(k, 128)) > kMaxGroups ||
-      count * (1 + ceil_div(n, 256) + ceil_div(k, 256)) > kMaxGroups)
+      (m / w.piece + count) * (ceil_div(n, 128) + ceil_div(k, 128)) > kMaxGroups)
     return XPOSE_EINVAL;
   const bool some = m && rank && count;
   Ranges r;
@@ -357,50 +351,29 @@ int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank, int64
 
   uint8_t *ws = (uint8_t *)workspace;
   const bool back = some && ((dx && k) || (da && k));  // dh is needed
-  if (weights || back) {
-    xpose::AdapterPrepArgs p{};
-    p.a = a;
-    p.b = b;
-    p.at = back && dx ? ws + w.at : nullptr;
-    p.bt = back ? ws + w.bt : nullptr;
-    p.ids = ids;
-    p.order = weights ? (int32_t *)(ws + w.order) : nullptr;
-    p.starts = (int32_t *)(ws + w.starts);
-    p.m = m;
-    p.n = n;
-    p.k = k;
-    p.lda = lda;
-    p.stride_a = stride_a;
-    p.ldb = ldb;
-    p.stride_b = stride_b;
-    p.rank = (int32_t)rank;
-    p.count = (int32_t)count;
-    rc = hip(xpose::launch_adapter_prep(p, dtype, (hipStream_t)stream));
-    if (rc != XPOSE_OK) return rc;
-  }
   float *dh = (float *)(ws + w.dh);
-  if (back) {
+  if (weights || back) {
     xpose::ShrinkArgs s{};
     s.x = dout;
-    s.w = ws + w.bt;
+    s.w = b;
+    s.turned = true;
     s.ids = ids;
     s.scale = scale;
     s.alpha = alpha;
     s.scaled = true;
-    s.h = w.plan.slices > 1 ? (float *)(ws + w.slices) : dh;
+    s.h = back ? dh : nullptr;
+    s.order = weights ? (int32_t *)(ws + w.order) : nullptr;
+    s.starts = (int32_t *)(ws + w.starts);
     s.m = m;
     s.k = n;
     s.ldx = lddout;
-    s.ldw = n;
-    s.stride_w = rank * n;
-    s.slice = m * rank;
+    s.ldw = ldb;
+    s.stride_w = stride_b;
     s.rank = (int32_t)rank;
     s.count = (int32_t)count;
-    s.blocks_per_slice = w.plan.blocks_per_slice;
+    s.steps_per_slice = w.plan.steps_per_slice;
     s.slots = w.plan.slots;
     rc = hip(xpose::launch_shrink(s, w.plan, dtype, (hipStream_t)stream));
-    if (rc == XPOSE_OK && w.plan.slices > 1)
-      rc = hip(xpose::launch_slices({(const float *)(ws + w.slices), dh, m * rank, w.plan.slices}, (hipStream_t)stream));
     if (rc != XPOSE_OK) return rc;
   }
   if (copies) {
@@ -408,14 +381,15 @@ int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank, int64
     const xpose::ExpandPlan plan = xpose::expand_plan(m, k, used);
     xpose::ExpandArgs e{};
     e.h = dh;
-    e.w = ws + w.at;
+    e.w = a;
+    e.turned = true;
     e.ids = ids;
     e.base = base;
     e.out = dx;
     e.m = m;
     e.n = k;
-    e.ldw = rank;
-    e.stride_w = rank * k;
+    e.ldw = lda;
+    e.stride_w = stride_a;
     e.ld_base = ld_base;
     e.ld_out = lddx;
     e.slice = m * rank;
@@ -423,6 +397,7 @@ int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank, int64
     e.rank = (int32_t)rank;
     e.count = (int32_t)used;
     e.slots = plan.slots;
+  e.strips = (int32_t)plan.strips;
     e.alpha = 1.f;
     rc = hip(xpose::launch_expand(e, plan, dtype, dx_dtype, (hipStream_t)stream));
     if (rc != XPOSE_OK) return rc;

@@ -40,37 +40,33 @@ hipError_t launch_rms_norm_backward(const RmsNormBwdArgs &, int dtype, hipStream
 // ----- low-rank adapters (adapter_kernels.hip) ---------------------------------
 
 // h[row][r] = factor sum_c x[row][c] w[ids[row]][r][c]: zeros in rows without an
-// adapter.  factor: 1, or alpha scale[ids[row]] where `scaled`.
+// adapter.  factor: 1, or alpha scale[ids[row]] where `scaled`.  And, where
+// order is not null, the rows of each adapter.
 struct ShrinkArgs {
   const void *x, *w;
   const float *scale_x;  // of e4m3 x
   const int32_t *ids;
   const float *scale;
-  float *h;        // the first slice's sums
+  float *h;        // the first slice's sums; null: not wanted
+  int32_t *order, *starts;  // rows by adapter; where each adapter's begin (count + 1)
   int64_t m, k;
   int64_t ldx, ld_scale_x, ldw, stride_w;
   int64_t slice;   // floats from one slice's sums to the next's
   int32_t rank, count;
-  int32_t blocks_per_slice;  // of the ceil(k / 128) blocks
+  int32_t steps_per_slice;  // steps of 128 bytes of a row of x
   int32_t slots;   // workgroups of a tile and slice, adapters in turn
+  uint32_t tiles;  // of rows; set by the launch
   float alpha;
   bool scaled;
+  bool turned;     // w is (columns, rank) in memory
 };
 struct ShrinkPlan {
   int row_tiles;  // of 16, of a workgroup
-  int slots, slices, blocks_per_slice;
+  int slots, slices, steps_per_slice;
 };
-ShrinkPlan shrink_plan(int64_t m, int64_t k, int64_t rank, int64_t count);
+// x_size: bytes of an element of x.  whole: no slices.
+ShrinkPlan shrink_plan(int64_t m, int64_t k, int64_t rank, int64_t count, int x_size, bool whole);
 hipError_t launch_shrink(const ShrinkArgs &, const ShrinkPlan &, int dtype, hipStream_t);
-
-// out[i] = sum of `slices` slices of `in`
-struct SlicesArgs {
-  const float *in;
-  float *out;
-  int64_t count;
-  int32_t slices;
-};
-hipError_t launch_slices(const SlicesArgs &, hipStream_t);
 
 // out[row][c] = base[row][c] + alpha scale[ids[row]] sum_r h[row][r] w[ids[row]][c][r]
 struct ExpandArgs {
@@ -86,29 +82,18 @@ struct ExpandArgs {
   int32_t slices;
   int32_t rank, count;
   int32_t slots;
+  int32_t strips;  // of a workgroup's columns
+  int32_t tiles;   // of rows, of a workgroup; set by the launch
   float alpha;
+  bool turned;     // w is (rank, columns) in memory
 };
 struct ExpandPlan {
-  int row_tiles;
+  int waves_down;  // of a workgroup, 16 rows each
   int slots;
-  int64_t workgroups;
+  int64_t strips, tiles;
 };
 ExpandPlan expand_plan(int64_t m, int64_t n, int64_t count);
 hipError_t launch_expand(const ExpandArgs &, const ExpandPlan &, int dtype, int out_dtype, hipStream_t);
-
-// What the backward pass reads more than once, laid out for it: every B with
-// its columns along rows, every A with its rows along columns, and the rows of
-// each adapter in order.
-struct AdapterPrepArgs {
-  const void *a, *b;
-  void *at, *bt;     // (count, k, rank), (count, rank, n); null: not wanted
-  const int32_t *ids;
-  int32_t *order, *starts;  // rows by adapter; where each adapter's begin (count + 1); null: not wanted
-  int64_t m, n, k;
-  int64_t lda, stride_a, ldb, stride_b;
-  int32_t rank, count;
-};
-hipError_t launch_adapter_prep(const AdapterPrepArgs &, int dtype, hipStream_t);
 
 // da[l][r][c] = sum over l's rows of dh[row][r] x[row][c]
 // db[l][c][r] = alpha scale[l] sum over l's rows of dout[row][c] h[row][r]

@@ -228,7 +228,7 @@ std::vector<Tensor> adapters(const Tensor &x, const Tensor &a, const Tensor &b, 
   Tensor out = given ? *given : empty({m, n}, type, x), h, ws;
   const Matrix mo = matrix(out, "out");
   int64_t size = 0;
-  check(xpose_adapters_workspace(m, k, rank, count, hidden, &size), "xpose_adapters_workspace");
+  check(xpose_adapters_workspace(m, k, rank, count, (int)x.element_size(), hidden, &size), "xpose_adapters_workspace");
   if (hidden) h = empty({m, rank}, at::kFloat, x);
   if (size) ws = empty({size}, at::kByte, x);
   check(xpose_adapters(m, n, k, rank, count, x.data_ptr(), mx.ld, scale_x ? scale_x->data_ptr<float>() : nullptr,
