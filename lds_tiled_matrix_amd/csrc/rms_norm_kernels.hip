@@ -45,7 +45,9 @@ __device__ inline void sum8(Vec8<T> x, Vec8<T> res, int64_t cols, int64_t col, f
 }
 
 // As in layer norm, workgroups stay, with the weight in registers and the next
-// row's loads under way.
+// row's loads under way.  Memory bounds it: 8192 x 8192 bfloat16 with the residual
+// moves 537 MB in 95 us (5.6 TB/s; a copy reaches 6.3), 4096 x 8192 to e4m3
+// 236 MB in 43 us.
 template <typename T, Out OUT, bool RES, int TR, int NC, bool SHORT>
 __global__ __launch_bounds__(norm_threads(TR)) void rms_norm_kernel(RmsNormArgs a) {
   __shared__ float lds[2][TR > 64 ? TR / 64 : 1];
@@ -161,6 +163,13 @@ hipError_t launch_rms(const RmsNormArgs &a, hipStream_t s) {
     else
       n = 1;
   }
+  // Long rows that leave as a tensor keep memory busy with half of that, and more
+  // rows at a time cost it: with the residual 8192 x 8192 bfloat16 takes 95 us and
+  // 99 with all, 3001 x 2999 float32 28 and 30, 4096 x 4096 bfloat16 23.5 and 25,
+  // without it 16384 x 2048 bfloat16 24 and 27.  Not where one workgroup would be
+  // left with idle lanes (12345 x 6789 bfloat16 158 and 151), and to e4m3 the
+  // arithmetic needs them all (4096 x 8192 53 and 43).
+  if (OUT == kTensor && TR > 64 && (n > 2 || a.cols == TR * NC * 8)) n = (n + 1) / 2;
   const int64_t grid = (a.rows + per - 1) / per, most = 256 * (int64_t)n;
   return launch(kernel, a, dim3((uint32_t)(grid < most ? grid : most)), norm_threads(TR), s);
 }
@@ -411,13 +420,15 @@ hipError_t launch_rms_norm_quantize(const RmsNormArgs &a, int dtype, bool pow2, 
 }
 
 // Workgroups, each with a row of sums in the workspace: as for layer norm's
-// backward pass, which weighs the same loads against twice the sums.
+// backward pass, but that half as many do for rows of over 2048 columns
+// (8192 x 4096 bfloat16 with the residual 48 us with 256, 52 with 512; 16384 x
+// 4096 float32 144 and 153; but 16384 x 2048 bfloat16 65 and 45).
 int rms_norm_bwd_parts(int64_t rows, int64_t cols) {
   if (cols <= 1024) {
     const int64_t per = cols <= 256 ? 16 : 4, parts = (rows + per - 1) / per;
     return (int)(parts < 256 ? parts : parts < 8 * 256 ? 256 : 512);
   }
-  const int64_t most = cols <= 4096 ? 512 : 256;
+  const int64_t most = cols <= 2048 ? 512 : 256;
   int64_t parts = 1;
   while (parts < most && parts * parts < 32 * rows) parts *= 2;
   return (int)(rows < parts ? rows : parts);
