@@ -89,8 +89,7 @@ int xpose_rms_norm_backward_workspace(int64_t rows, int64_t cols,
  * rounded once.  Where hidden or B holds an infinity, what it goes into is
  * infinite or NaN.  Nothing of a row goes into another one.
  *
- * m <= 2^27, n and k <= 2^31 - 1, rank <= 4096, count <= 65535, and no launch
- * of over 2^24 - 1 workgroups: about m n <= 2^35. */
+ * m <= 2^26, n and k <= 2^30, rank <= 4096, count <= 65535. */
 int xpose_adapters(int64_t m, int64_t n, int64_t k, int64_t rank,
                    int64_t count, const void *x, int64_t ldx,
                    const float *scale_x, int64_t ld_scale_x, const void *a,
@@ -116,8 +115,8 @@ int xpose_adapters_workspace(int64_t m, int64_t k, int64_t rank, int64_t count,
  * dx_dtype, dtype or XPOSE_F32; dx may be base itself (same pitch).  da and db:
  * dense float32 of count x rank x k and count x n x rank, zeros for adapters of
  * no row.  dx, da and db may each be NULL: not wanted.  Sums are float32, in an
- * order of their own for each set of sizes and ids.  Limits as above, for m n
- * and m k, and (m / 64 + count) (ceil(n / 128) + ceil(k / 128)) < 2^24. */
+ * order of their own for each set of sizes and ids.  Limits as above, and
+ * (m / 4096 + count + 1) (ceil(n / 128) + ceil(k / 128)) < 2^23 - 768. */
 int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank,
                             int64_t count, const void *dout, int64_t lddout,
                             const void *x, int64_t ldx, const void *a,

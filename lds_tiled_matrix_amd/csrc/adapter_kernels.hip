@@ -192,13 +192,17 @@ __device__ __forceinline__ void each_adapter(int id, int slot, int slots, F &&f)
 //
 // The instruction wants another row in each of 16 neighbouring lanes.  Loaded
 // so, every lane is a memory request of its own, and a compute unit gets 16
-// bytes a cycle (measured 36 GB/s, from the caches too; 4001 x 4096 bfloat16
-// took 18 us).  So 8 lanes load 128 bytes of a row (100 to 120 GB/s), two steps
-// ahead, and the step goes through the wave's own piece of LDS: no barriers.  A
-// row's 8 chunks there are permuted by an exclusive or with bits 1 to 3 of the
-// row, which spreads the reads of 16 rows over all banks.  Weights that come with
-// the rank along their rows (WT, B in the backward pass) are turned around by
-// the reads.
+// bytes a cycle (measured 36 GB/s, from the caches too).  So 8 lanes load 128
+// bytes of a row (100 to 120 GB/s), two or four steps ahead, and the step goes
+// through the wave's own piece of LDS: no barriers.  A row's 8 chunks there are
+// permuted by an exclusive or with bits 1 to 3 of the row, which spreads the
+// reads of 16 rows over all banks.  Weights that come with the rank along their
+// rows (WT, B in the backward pass) are turned around by the reads.
+//
+// Reading x bounds it with many rows, the latency of a few steps with few: 4001 x
+// 4096 bfloat16, rank 16, take 13.5 us (2.4 TB/s, of x and once a tile of A from
+// the caches; 18 with the rows' own loads), 8192 x 4096 turned 23 us (2.9 TB/s),
+// 16 tokens of 16 adapters 5.5 us.
 template <typename T, bool Q> using ShrinkX = typename std::conditional<Q, uint8_t, T>::type;
 constexpr int kShrinkWaves = 8, kShrinkThreads = 64 * kShrinkWaves;
 
@@ -581,7 +585,8 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(ShrinkArgs a) {
 // (columns of out) as the second: a lane has four rows of one column.  Which of
 // the columns of eight instructions is which of their rows is chosen so that a
 // lane has 16 bytes of each of its rows, and 16 lanes 256: with a row a lane
-// instead, as in `shrink` above, 4001 x 8192 bfloat16 took 41 us.
+// instead, as in `shrink` above, 4001 x 8192 bfloat16 took 41 us, and so 32 (4.1
+// TB/s of base and out, which bound it: copies reach 6.3).
 //
 // A workgroup has WR waves of 16 rows under each other and 4 / WR side by side,
 // 128 columns each, and goes down the rows, the next tile's ids, base and h on
@@ -649,16 +654,18 @@ template <> __device__ inline f32x4 multiply_split<float>(const Vec8<float> &w, 
   return sum;
 }
 
+// An operand's 64 lanes follow each other, 16 bytes each (float32: twice), a
+// bank group on from the previous operand's.
+template <typename T> constexpr int kOperandBytes = 1024 * (int)sizeof(Vec8<T>) / 16 + 16;
+template <typename T, int WR> constexpr int kExpandLds = kExpandCols * kExpandWaves / WR / 16 * kOperandBytes<T>;
+
 template <typename T, typename O, int WR, bool WT, bool SHORT>
-__global__ __launch_bounds__(kExpandThreads) void expand_kernel(ExpandArgs a) {
+__device__ __forceinline__ void expand(const ExpandArgs &a, uint32_t block, uint8_t *lds) {
   constexpr int V = kChunk<O>, P = 8 / V, ROWS = 16 * WR, COLS = kExpandCols * kExpandWaves / WR;
-  // An operand's 64 lanes follow each other, 16 bytes each (float32: twice), a
-  // bank group on from the previous operand's.
-  constexpr int C = (int)sizeof(Vec8<T>) / 16, kOperand = 1024 * C + 16;
-  __shared__ __align__(16) uint8_t lds[COLS / 16 * kOperand];
+  constexpr int C = (int)sizeof(Vec8<T>) / 16, kOperand = kOperandBytes<T>;
   const int tid = threadIdx.x, lane = tid % 64, i16 = lane % 16, g = lane / 16;
   const int wave = scalar(tid / 64);
-  const int slot = scalar(blockIdx.x % a.slots), place = scalar(blockIdx.x / a.slots);
+  const int slot = scalar(block % a.slots), place = scalar(block / a.slots);
   const int first = scalar(place / a.strips) * a.tiles, last = scalar(min(first + a.tiles, (int)((a.m + ROWS - 1) / ROWS)));
   const int64_t n0 = (int64_t)scalar(place % a.strips) * COLS;
   const int side = wave / WR;      // of the waves side by side
@@ -824,6 +831,12 @@ __global__ __launch_bounds__(kExpandThreads) void expand_kernel(ExpandArgs a) {
   }
 }
 
+template <typename T, typename O, int WR, bool WT, bool SHORT>
+__global__ __launch_bounds__(kExpandThreads) void expand_kernel(ExpandArgs a) {
+  __shared__ __align__(16) uint8_t lds[kExpandLds<T, WR>];
+  expand<T, O, WR, WT, SHORT>(a, blockIdx.x, lds);
+}
+
 // ----- the adapters' gradients ----------------------------------------------------------
 //
 // G[r][c] = sum over rows u[row][r] v[row][c], u of r columns in float32, v as
@@ -835,7 +848,11 @@ __global__ __launch_bounds__(kExpandThreads) void expand_kernel(ExpandArgs a) {
 // the workspace and a second launch adds them up, in their order.  Adapter l's
 // pieces are the numbers starts[l] / piece + l and on: there are enough
 // numbers between one adapter's first and the next one's.  Workspace slots,
-// which only adapters of over a piece need, are 2 (starts[l] / piece) and on.
+// which only adapters of over a piece need, are 2 (starts[l] / piece) and on: an
+// adapter of p > 1 pieces has over (p - 1) piece rows, so the next one's first
+// slot is 2 (p - 1) >= p further at least.
+//
+// Reading x and dout bounds it, once for each 64 ranks.
 constexpr int kGradThreads = 256, kGradCols = 128, kGradWaves = 4;
 
 __device__ inline int grad_pieces(int rows, int piece) { return (rows + piece - 1) / piece; }
@@ -846,12 +863,12 @@ template <typename T, int NR> struct GradRows {
 };
 
 template <typename T, int NR, bool SHORT>
-__global__ __launch_bounds__(kGradThreads) void adapter_grad_kernel(AdapterGradArgs a, int tiles_k, int tiles) {
+__device__ __forceinline__ void adapter_grad(const AdapterGradArgs &a, uint32_t block, f32x4 (*lds)[8][64]) {
   constexpr int DEPTH = NR * (int)sizeof(T) <= 4 ? 3 : 2;  // blocks of rows under way, as registers allow
-  __shared__ f32x4 lds[NR][8][64];
+  const int tiles_k = a.tiles_k, tiles = a.tiles;
   const int tid = threadIdx.x, lane = tid % 64, i16 = lane % 16, g = lane / 16;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
-  const int number = scalar((int)(blockIdx.x / (uint32_t)tiles)), tile = scalar((int)(blockIdx.x % (uint32_t)tiles));
+  const int number = scalar((int)(block / (uint32_t)tiles)), tile = scalar((int)(block % (uint32_t)tiles));
   const int r0 = blockIdx.y * 16 * NR;
   // the last adapter whose first number is no later, by 64 of them at a time
   int l = 0;
@@ -905,11 +922,10 @@ __global__ __launch_bounds__(kGradThreads) void adapter_grad_kernel(AdapterGradA
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  // `whole`: all 16 rows are this piece's; else those past it may hold anything
-  auto multiply = [&](int p0, GradRows<T, NR> &rows, auto whole) {
+  auto multiply = [&](int p0, GradRows<T, NR> &rows) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const bool in = decltype(whole)::value || p0 + 4 * s + g < end;
+      const bool in = p0 + 4 * s + g < end;  // rows past the piece may hold anything
       if constexpr (!SHORT) settle8<T>(rows.v[s], cols, col);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -932,8 +948,7 @@ __global__ __launch_bounds__(kGradThreads) void adapter_grad_kernel(AdapterGradA
 #pragma unroll
       for (int d = 0; d < DEPTH; ++d) {
         const int at = p0 + d * kApart;
-        if (at + 16 <= end) multiply(at, rows_of[d], std::true_type{});
-        else if (at < end) multiply(at, rows_of[d], std::false_type{});
+        multiply(at, rows_of[d]);
         load(numbers[d], at + 2 * DEPTH * kApart, rows_of[d]);
       }
   }
@@ -966,6 +981,27 @@ __global__ __launch_bounds__(kGradThreads) void adapter_grad_kernel(AdapterGradA
       if (c < here) to[(int64_t)(r0 + r) * a.k + c0 + c] = value(r, c);
     }
   }
+}
+
+template <typename T, int NR, bool SHORT>
+__global__ __launch_bounds__(kGradThreads) void adapter_grad_kernel(AdapterGradArgs a) {
+  __shared__ f32x4 lds[NR][8][64];
+  adapter_grad<T, NR, SHORT>(a, blockIdx.x, lds);
+}
+
+// dx and the adapters' gradients in one launch, which need nothing of each other,
+// a workgroup of each in turn: 8192 rows, 4096 columns both ways, bfloat16 take
+// 92 us a pass, 96 with one after the other and 98 in two launches, 300 rows 23
+// and 28.
+template <typename T, typename O, int NR, bool SHORT>
+__global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NR < 4 ? 2 : 1) void adapter_both_kernel(ExpandArgs e, AdapterGradArgs g, uint32_t expands) {
+  constexpr int kBytes = kExpandLds<T, 4> > NR * 8192 ? kExpandLds<T, 4> : NR * 8192;
+  __shared__ __align__(16) uint8_t lds[kBytes];
+  const uint32_t grads = gridDim.x - expands, pairs = min(expands, grads), block = blockIdx.x;
+  const bool grad = block < 2 * pairs ? block % 2 : grads > expands;
+  const uint32_t number = block < 2 * pairs ? block / 2 : block - pairs;
+  if (grad) adapter_grad<T, NR, SHORT>(g, number, reinterpret_cast<f32x4 (*)[8][64]>(lds));
+  else if (blockIdx.y == 0) expand<T, O, 4, true, SHORT>(e, number, lds);
 }
 
 // Adapters of several pieces get their sum.
@@ -1050,7 +1086,7 @@ template <typename T, bool Q, int NI, bool WT>
 hipError_t shrink_rank(const ShrinkArgs &a, const ShrinkPlan &p, hipStream_t s) {
   // weights take 16 registers a rank and step, twice that next to e4m3, four
   // times in float32 next to e4m3: more would spill
-  constexpr int most = Q ? (sizeof(T) == 2 && NI == 1 ? 2 : 1) : sizeof(T) == 2 && NI == 1 && !WT ? 4 : 2;
+  constexpr int most = Q ? (sizeof(T) == 2 && NI == 1 ? 2 : 1) : sizeof(T) == 2 && !WT ? 4 : 2;
   if constexpr (WT)
     if (a.rank < kChunk<T>) return shrink<T, Q, NI, 1, WT, true>(a, p, s);
   if (a.rank <= 16 || most == 1) return shrink<T, Q, NI, 1, WT, false>(a, p, s);
@@ -1059,7 +1095,7 @@ hipError_t shrink_rank(const ShrinkArgs &a, const ShrinkPlan &p, hipStream_t s) 
 }
 template <typename T, bool Q, bool WT>
 hipError_t shrink(ShrinkArgs a, const ShrinkPlan &p, hipStream_t s) {
-  constexpr int most = Q && sizeof(T) == 4 ? 1 : 2;
+  constexpr int most = Q && sizeof(T) == 2 ? 2 : 1;
   const int64_t rows = 16 * std::min(p.row_tiles, most);
   a.tiles = a.h ? (uint32_t)((a.m + rows - 1) / rows) : 0;
   return p.row_tiles == 1 ? shrink_rank<T, Q, 1, WT>(a, p, s) : shrink_rank<T, Q, most, WT>(a, p, s);
@@ -1069,24 +1105,34 @@ hipError_t shrink(const ShrinkArgs &a, const ShrinkPlan &p, hipStream_t s) {
   return a.turned ? shrink<T, false, true>(a, p, s) : a.scale_x ? shrink<T, true, false>(a, p, s) : shrink<T, false, false>(a, p, s);
 }
 
-template <typename T, typename O, int WR, bool WT, bool SHORT>
-hipError_t expand(ExpandArgs a, const ExpandPlan &p, hipStream_t s) {
-  const void *kernel = reinterpret_cast<const void *>(&expand_kernel<T, O, WR, WT, SHORT>);
-  // tiles of a workgroup: as many workgroups as run at once (4001 x 8192 bfloat16,
-  // two of a compute unit: 44 us with 8 tiles, 49 with 6, 54 with one)
+// How many workgroups of a kernel run at once.
+template <typename Tag>
+int64_t groups_at_once(const void *kernel, int threads) {
   static std::atomic<int> at_once{0};  // of a compute unit; kept once it is known
   int n = at_once.load(std::memory_order_relaxed);
   if (n == 0) {
-    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kExpandThreads, 0) == hipSuccess && n > 0)
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) == hipSuccess && n > 0)
       at_once.store(n, std::memory_order_relaxed);
     else
       n = 1;
   }
-  const int64_t most = 256 * (int64_t)n, side = (int64_t)a.strips * a.slots;
-  const int64_t down = std::max<int64_t>(1, most / side);
+  return 256 * (int64_t)n;
+}
+// Tiles of a workgroup, for as many workgroups as run at once (4001 x 8192
+// bfloat16, two of a compute unit: 44 us with 8 tiles, 49 with 6, 54 with one);
+// how many there are then.
+uint32_t deal_out(ExpandArgs &a, const ExpandPlan &p, int64_t at_once) {
+  const int64_t side = (int64_t)a.strips * a.slots, down = std::max<int64_t>(1, at_once / side);
   a.tiles = (int32_t)((p.tiles + down - 1) / down);
-  const int64_t groups = (p.tiles + a.tiles - 1) / a.tiles * side;
-  return launch(kernel, dim3((uint32_t)groups), kExpandThreads, s, a);
+  return (uint32_t)((p.tiles + a.tiles - 1) / a.tiles * side);
+}
+
+template <typename T, typename O, int WR, bool WT, bool SHORT>
+hipError_t expand(ExpandArgs a, const ExpandPlan &p, hipStream_t s) {
+  struct Tag;
+  const void *kernel = reinterpret_cast<const void *>(&expand_kernel<T, O, WR, WT, SHORT>);
+  const uint32_t groups = deal_out(a, p, groups_at_once<Tag>(kernel, kExpandThreads));
+  return launch(kernel, dim3(groups), kExpandThreads, s, a);
 }
 template <typename T, typename O, bool WT, bool SHORT>
 hipError_t expand(const ExpandArgs &a, const ExpandPlan &p, hipStream_t s) {
@@ -1102,37 +1148,77 @@ hipError_t expand(const ExpandArgs &a, const ExpandPlan &p, hipStream_t s) {
   return a.turned ? expand<T, O, true>(a, p, s) : expand<T, O, false>(a, p, s);
 }
 
-template <typename T, bool SHORT>
-const void *grad_kernel(int nr) {
-  return nr == 1   ? reinterpret_cast<const void *>(&adapter_grad_kernel<T, 1, SHORT>)
-         : nr == 2 ? reinterpret_cast<const void *>(&adapter_grad_kernel<T, 2, SHORT>)
-                   : reinterpret_cast<const void *>(&adapter_grad_kernel<T, 4, SHORT>);
+// The gradients' launch: its workgroups, columns of tiles and operands.
+struct GradGrid {
+  uint32_t groups, chunks;
+  int nr;
+  bool narrow;  // columns shorter than a load
+};
+GradGrid grad_grid(AdapterGradArgs &a) {
+  a.tiles_k = a.da ? (int)((a.k + kGradCols - 1) / kGradCols) : 0;
+  a.tiles = a.tiles_k + (a.db ? (int)((a.n + kGradCols - 1) / kGradCols) : 0);
+  GradGrid g{};
+  g.nr = a.rank <= 16 ? 1 : a.rank <= 32 ? 2 : 4;
+  g.groups = (uint32_t)((a.m / a.piece + a.count) * a.tiles);
+  g.chunks = (uint32_t)((a.rank + 16 * g.nr - 1) / (16 * g.nr));
+  g.narrow = (a.da && a.k < 8) || (a.db && a.n < 8);
+  return g;
 }
-template <typename T>
-hipError_t grad(const AdapterGradArgs &a, hipStream_t s) {
-  const int tiles_k = a.da ? (int)((a.k + kGradCols - 1) / kGradCols) : 0;
-  const int tiles = tiles_k + (int)(a.db ? (a.n + kGradCols - 1) / kGradCols : 0);
-  const int64_t numbers = a.m / a.piece + a.count;
-  if (tiles == 0) return hipSuccess;
-  const int nr = a.rank <= 16 ? 1 : a.rank <= 32 ? 2 : 4;
-  const dim3 grid((uint32_t)(numbers * tiles), (uint32_t)((a.rank + 16 * nr - 1) / (16 * nr)));
-  const bool narrow = (a.da && a.k < 8) || (a.db && a.n < 8);
-  const void *kernel = narrow ? grad_kernel<T, true>(nr) : grad_kernel<T, false>(nr);
-  const hipError_t e = launch(kernel, grid, kGradThreads, s, a, tiles_k, tiles);
-  if (e != hipSuccess || a.m <= a.piece) return e;  // no adapter has two pieces
+hipError_t grad_sum(const AdapterGradArgs &a, hipStream_t s) {
+  if (a.m <= a.piece) return hipSuccess;  // no adapter has two pieces
   const int64_t values = (int64_t)a.rank * (a.k + a.n), most = 4096 / a.count + 1;
   const int64_t groups = std::min((values + kGradThreads - 1) / kGradThreads, most);
   return launch(reinterpret_cast<const void *>(&adapter_grad_sum_kernel), dim3((uint32_t)(groups * a.count)),
                 kGradThreads, s, a, groups);
+}
+template <typename T, bool SHORT>
+hipError_t grad(const AdapterGradArgs &a, const GradGrid &g, hipStream_t s) {
+  const void *kernel = g.nr == 1   ? reinterpret_cast<const void *>(&adapter_grad_kernel<T, 1, SHORT>)
+                       : g.nr == 2 ? reinterpret_cast<const void *>(&adapter_grad_kernel<T, 2, SHORT>)
+                                   : reinterpret_cast<const void *>(&adapter_grad_kernel<T, 4, SHORT>);
+  return launch(kernel, dim3(g.groups, g.chunks), kGradThreads, s, a);
+}
+template <typename T>
+hipError_t grad(AdapterGradArgs a, hipStream_t s) {
+  const GradGrid g = grad_grid(a);
+  if (g.groups == 0) return hipSuccess;
+  const hipError_t e = g.narrow ? grad<T, true>(a, g, s) : grad<T, false>(a, g, s);
+  return e == hipSuccess ? grad_sum(a, s) : e;
+}
+
+template <typename T, typename O, int NR, bool SHORT>
+hipError_t both(ExpandArgs e, const ExpandPlan &p, const AdapterGradArgs &a, const GradGrid &g, hipStream_t s) {
+  struct Tag;
+  const void *kernel = reinterpret_cast<const void *>(&adapter_both_kernel<T, O, NR, SHORT>);
+  const uint32_t expands = deal_out(e, p, groups_at_once<Tag>(kernel, kGradThreads));
+  return launch(kernel, dim3(expands + g.groups, g.chunks), kGradThreads, s, e, a, expands);
+}
+template <typename T, typename O, bool SHORT>
+hipError_t both(const ExpandArgs &e, const ExpandPlan &p, const AdapterGradArgs &a, const GradGrid &g, hipStream_t s) {
+  return g.nr == 1   ? both<T, O, 1, SHORT>(e, p, a, g, s)
+         : g.nr == 2 ? both<T, O, 2, SHORT>(e, p, a, g, s)
+                     : both<T, O, 4, SHORT>(e, p, a, g, s);
+}
+template <typename T, typename O>
+hipError_t both(const ExpandArgs &e, const ExpandPlan &p, AdapterGradArgs a, hipStream_t s) {
+  const GradGrid g = grad_grid(a);
+  const hipError_t err = g.narrow || e.n < 8 || e.rank < 8 ? both<T, O, true>(e, p, a, g, s) : both<T, O, false>(e, p, a, g, s);
+  return err == hipSuccess ? grad_sum(a, s) : err;
 }
 
 }  // namespace
 
 ShrinkPlan shrink_plan(int64_t m, int64_t k, int64_t rank, int64_t count, int x_size, bool whole) {
   ShrinkPlan p{};
-  p.row_tiles = m <= 4096 ? 1 : 2;
+  // e4m3 rows take twice their bytes of weights: 32 of them a workgroup from where
+  // those still fill the card (4096 columns, rank 16, 8192 rows 18.5 and 23 us,
+  // 16384 rows 32 and 40; but bfloat16 25 and 24, 5000 rows 25 and 21)
+  p.row_tiles = x_size == 1 && m > 4096 ? 2 : 1;
   const int64_t tiles = (m + 16 * p.row_tiles - 1) / (16 * p.row_tiles);
-  // a tile's rows have 16 adapters at most
+  // Few tiles: their adapters (16 of a tile at most) side by side, up to a
+  // workgroup each, and the columns in up to four slices, which `expand` adds up
+  // (16 rows of 16 adapters, 4096 columns, both launches: 24 us with one slot, 14.5
+  // with 4, 12 with 16; then 12.8 with one slice, 11.9 with 2, 11.7 with 4).
   const int64_t adapters = std::min<int64_t>(std::min<int64_t>(m, 16), count);
   p.slots = 1;
   while (p.slots < adapters && tiles * p.slots < 64) p.slots *= 2;
@@ -1147,13 +1233,13 @@ hipError_t launch_shrink(const ShrinkArgs &a, const ShrinkPlan &p, int dtype, hi
   return dtype == XPOSE_F32 ? shrink<float>(a, p, s) : dtype == XPOSE_F16 ? shrink<_Float16>(a, p, s) : shrink<__bf16>(a, p, s);
 }
 
-ExpandPlan expand_plan(int64_t m, int64_t n, int64_t count) {
+ExpandPlan expand_plan(int64_t m, int64_t n, int64_t count, bool beside) {
   ExpandPlan p{};
-  p.waves_down = m > 16 ? 4 : 1;
+  p.waves_down = m > 16 || beside ? 4 : 1;
   const int rows = 16 * p.waves_down, cols = kExpandCols * kExpandWaves / p.waves_down;
   p.strips = (n + cols - 1) / cols;
   p.tiles = (m + rows - 1) / rows;
-  // a tile's rows have so many adapters at most
+  // side by side as in shrink_plan; a tile's rows have so many adapters at most
   const int64_t adapters = std::min(std::min(m, (int64_t)rows), count);
   p.slots = 1;
   while (p.slots < adapters && p.tiles * p.strips * p.slots < 256) p.slots *= 2;
@@ -1168,12 +1254,21 @@ hipError_t launch_expand(const ExpandArgs &a, const ExpandPlan &p, int dtype, in
 
 int adapter_grad_piece(int64_t m, int64_t n, int64_t k) {
   const int64_t tiles = (n + kGradCols - 1) / kGradCols + (k + kGradCols - 1) / kGradCols;
-  if (m <= 512) return 512;  // one piece an adapter: no second launch
+  if (m <= 512) return 512;  // one piece an adapter: no second launch (300 rows 28 and 23 us a pass)
+  // three workgroups a compute unit or fewer (8192 rows, 4096 columns both ways: 128
+  // rows a piece 128 us, 256 111, 512 104, 1024 101, 2048 117)
   int piece = 128;
   while (piece < 4096 && m / piece * tiles > 768) piece *= 2;
   return piece;
 }
 int64_t adapter_grad_slots(int64_t m, int piece) { return m > piece ? 2 * (m / piece + 1) : 0; }
+hipError_t launch_adapter_both(const ExpandArgs &e, const ExpandPlan &p, const AdapterGradArgs &a, int dtype,
+                               int dx_dtype, hipStream_t s) {
+  if (dtype == XPOSE_F32) return both<float, float>(e, p, a, s);
+  if (dtype == XPOSE_F16)
+    return dx_dtype == XPOSE_F32 ? both<_Float16, float>(e, p, a, s) : both<_Float16, _Float16>(e, p, a, s);
+  return dx_dtype == XPOSE_F32 ? both<__bf16, float>(e, p, a, s) : both<__bf16, __bf16>(e, p, a, s);
+}
 hipError_t launch_adapter_grad(const AdapterGradArgs &a, int dtype, hipStream_t s) {
   return dtype == XPOSE_F32 ? grad<float>(a, s) : dtype == XPOSE_F16 ? grad<_Float16>(a, s) : grad<__bf16>(a, s);
 }
@@ -1189,7 +1284,11 @@ hipError_t launch_dropout(const DropoutArgs &given, int dtype, hipStream_t s) {
   a.lanes = kDropThreads;
   while (a.lanes / 2 >= chunks) a.lanes /= 2;
   const int64_t wide = (chunks + a.lanes - 1) / a.lanes, at_once = kDropThreads / a.lanes;
-  const int64_t groups = std::min<int64_t>((a.rows + at_once - 1) / at_once, std::max<int64_t>(1, 4096 / wide));
+  // A row a lane and short workgroups, which go through memory in order: 8192 x
+  // 8192 bfloat16 with the residual takes 71 us, 77 where 4096 workgroups stay,
+  // float32 134 and 146 (100000 x 128 bfloat16 14.3 and 14.4).
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(65535, ((int64_t)1 << 24) / wide - 1));
+  const int64_t groups = std::min((a.rows + at_once - 1) / at_once, most);
   const dim3 grid((uint32_t)wide, (uint32_t)groups);
   return dtype == XPOSE_F32 ? dropout<float>(a, grid, s) : dtype == XPOSE_F16 ? dropout<_Float16>(a, grid, s) : dropout<__bf16>(a, grid, s);
 }

@@ -15,8 +15,11 @@
 
 namespace {
 
-constexpr int64_t kMaxAdapterRows = (int64_t)1 << 27, kMaxRank = 4096, kMaxAdapters = 65535;
-constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1;  // of a launch
+// Under 2^32 threads of a launch: 512 for 16 rows and for an adapter's list; 256
+// for 128 columns of n or k, at least, and as many workgroups again beside them.
+constexpr int64_t kMaxAdapterRows = (int64_t)1 << 26, kMaxAdapterCols = (int64_t)1 << 30;
+constexpr int64_t kMaxRank = 4096, kMaxAdapters = 65535;
+constexpr int64_t kMaxGradGroups = (int64_t)1 << 23;
 
 // Parts of a workspace, one after the other, each at a multiple of 16 bytes.
 class Parts {
@@ -177,14 +180,8 @@ int xpose_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t 
 // ----- low-rank adapters --------------------------------------------------------------
 
 static bool adapter_sizes(int64_t m, int64_t n, int64_t k, int64_t rank, int64_t count) {
-  return m >= 0 && n >= 0 && k >= 0 && rank >= 0 && count >= 0 && m <= kMaxAdapterRows && n <= INT32_MAX &&
-         k <= INT32_MAX && rank <= kMaxRank && count <= kMaxAdapters;
-}
-
-static bool expand_fits(int64_t m, int64_t n, int64_t count) {
-  if (m == 0 || n == 0) return true;
-  const xpose::ExpandPlan p = xpose::expand_plan(m, n, count);
-  return p.tiles * p.strips * p.slots <= kMaxGroups;
+  return m >= 0 && n >= 0 && k >= 0 && rank >= 0 && count >= 0 && m <= kMaxAdapterRows && n <= kMaxAdapterCols &&
+         k <= kMaxAdapterCols && rank <= kMaxRank && count <= kMaxAdapters;
 }
 
 int xpose_adapters_workspace(int64_t m, int64_t k, int64_t rank, int64_t count, int32_t x_size, int32_t hidden,
@@ -203,7 +200,7 @@ int xpose_adapters(int64_t m, int64_t n, int64_t k, int64_t rank, int64_t count,
                    const void *b, int64_t ldb, int64_t stride_b, int32_t dtype, const int32_t *ids, const float *scale,
                    float alpha, const void *base, int64_t ld_base, void *out, int64_t ld_out, int32_t out_dtype,
                    float *hidden, void *workspace, int64_t workspace_bytes, void *stream) {
-  if (!adapter_sizes(m, n, k, rank, count) || workspace_bytes < 0 || !expand_fits(m, n, count)) return XPOSE_EINVAL;
+  if (!adapter_sizes(m, n, k, rank, count) || workspace_bytes < 0) return XPOSE_EINVAL;
   const int size = size_of(dtype), out_size = size_of(out_dtype);
   if (!size || !out_size || (out_dtype != dtype && out_dtype != XPOSE_F32)) return XPOSE_EDTYPE;
   const int x_size = scale_x ? 1 : size;
@@ -255,7 +252,7 @@ int xpose_adapters(int64_t m, int64_t n, int64_t k, int64_t rank, int64_t count,
   }
   if (n == 0 || ((rank == 0 || count == 0) && base == out)) return XPOSE_OK;
   const int64_t used = rank ? count : 0;  // with no rank, no row has an adapter
-  const xpose::ExpandPlan plan = xpose::expand_plan(m, n, used);
+  const xpose::ExpandPlan plan = xpose::expand_plan(m, n, used, false);
   xpose::ExpandArgs e{};
   e.h = h;
   e.w = b;
@@ -287,6 +284,8 @@ struct BackwardParts {
   int piece;
 };
 bool backward_parts(int64_t m, int64_t n, int64_t k, int64_t rank, int64_t count, int size, BackwardParts &w) {
+  // pieces of 4096 rows, or shorter ones, 768 workgroups at most
+  if ((m / 4096 + count + 1) * (ceil_div(n, 128) + ceil_div(k, 128)) >= kMaxGradGroups - 768) return false;
   Parts p;
   w.plan = xpose::shrink_plan(std::max<int64_t>(m, 1), n, rank, count, size, true);
   w.piece = xpose::adapter_grad_piece(m, n, k);
@@ -316,14 +315,11 @@ int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank, int64
                             const float *scale, float alpha, const float *hidden, const void *base, int64_t ld_base,
                             void *dx, int64_t lddx, int32_t dx_dtype, float *da, float *db, void *workspace,
                             int64_t workspace_bytes, void *stream) {
-  if (!adapter_sizes(m, n, k, rank, count) || workspace_bytes < 0 || (dx && !expand_fits(m, k, count)))
-    return XPOSE_EINVAL;
+  if (!adapter_sizes(m, n, k, rank, count) || workspace_bytes < 0) return XPOSE_EINVAL;
   const int size = size_of(dtype), dx_size = size_of(dx_dtype);
   if (!size || !dx_size || (dx_dtype != dtype && dx_dtype != XPOSE_F32)) return XPOSE_EDTYPE;
   BackwardParts w;
-  if (!backward_parts(m, n, k, rank, count, size, w) ||
-      (m / w.piece + count) * (ceil_div(n, 128) + ceil_div(k, 128)) > kMaxGroups)
-    return XPOSE_EINVAL;
+  if (!backward_parts(m, n, k, rank, count, size, w)) return XPOSE_EINVAL;
   const bool some = m && rank && count;
   Ranges r;
   r.matrix(dout, some ? m : 0, n, lddout, size, size, false);
@@ -376,33 +372,30 @@ int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank, int64
     rc = hip(xpose::launch_shrink(s, w.plan, dtype, (hipStream_t)stream));
     if (rc != XPOSE_OK) return rc;
   }
-  if (copies) {
-    const int64_t used = some ? count : 0;
-    const xpose::ExpandPlan plan = xpose::expand_plan(m, k, used);
-    xpose::ExpandArgs e{};
-    e.h = dh;
-    e.w = a;
-    e.turned = true;
-    e.ids = ids;
-    e.base = base;
-    e.out = dx;
-    e.m = m;
-    e.n = k;
-    e.ldw = lda;
-    e.stride_w = stride_a;
-    e.ld_base = ld_base;
-    e.ld_out = lddx;
-    e.slice = m * rank;
-    e.slices = 1;
-    e.rank = (int32_t)rank;
-    e.count = (int32_t)used;
-    e.slots = plan.slots;
+  const int64_t used = some ? count : 0;
+  const bool beside = copies && weights;
+  const xpose::ExpandPlan plan = xpose::expand_plan(m, k, used, beside);
+  xpose::ExpandArgs e{};
+  e.h = dh;
+  e.w = a;
+  e.turned = true;
+  e.ids = ids;
+  e.base = base;
+  e.out = dx;
+  e.m = m;
+  e.n = k;
+  e.ldw = lda;
+  e.stride_w = stride_a;
+  e.ld_base = ld_base;
+  e.ld_out = lddx;
+  e.slice = m * rank;
+  e.slices = 1;
+  e.rank = (int32_t)rank;
+  e.count = (int32_t)used;
+  e.slots = plan.slots;
   e.strips = (int32_t)plan.strips;
-    e.alpha = 1.f;
-    rc = hip(xpose::launch_expand(e, plan, dtype, dx_dtype, (hipStream_t)stream));
-    if (rc != XPOSE_OK) return rc;
-  }
-  if (!weights) return XPOSE_OK;
+  e.alpha = 1.f;
+  if (!weights) return hip(xpose::launch_expand(e, plan, dtype, dx_dtype, (hipStream_t)stream));
   xpose::AdapterGradArgs g{};
   g.dh = dh;
   g.h = hidden;
@@ -411,8 +404,8 @@ int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank, int64
   g.order = (const int32_t *)(ws + w.order);
   g.starts = (const int32_t *)(ws + w.starts);
   g.scale = scale;
-  g.da = da;
-  g.db = db;
+  g.da = k ? da : nullptr;
+  g.db = n ? db : nullptr;
   g.partial = (float *)(ws + w.partial);
   g.m = m;
   g.n = n;
@@ -423,7 +416,8 @@ int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank, int64
   g.count = (int32_t)count;
   g.piece = w.piece;
   g.alpha = alpha;
-  return hip(xpose::launch_adapter_grad(g, dtype, (hipStream_t)stream));
+  return hip(beside ? xpose::launch_adapter_both(e, plan, g, dtype, dx_dtype, (hipStream_t)stream)
+                    : xpose::launch_adapter_grad(g, dtype, (hipStream_t)stream));
 }
 
 // ----- dropout ---------------------------------------------------------------------------

@@ -92,7 +92,8 @@ struct ExpandPlan {
   int slots;
   int64_t strips, tiles;
 };
-ExpandPlan expand_plan(int64_t m, int64_t n, int64_t count);
+// beside: for launch_adapter_both.
+ExpandPlan expand_plan(int64_t m, int64_t n, int64_t count, bool beside);
 hipError_t launch_expand(const ExpandArgs &, const ExpandPlan &, int dtype, int out_dtype, hipStream_t);
 
 // da[l][r][c] = sum over l's rows of dh[row][r] x[row][c]
@@ -108,11 +109,15 @@ struct AdapterGradArgs {
   int64_t ldx, lddout;
   int32_t rank, count;
   int32_t piece;     // rows of one workgroup
+  int32_t tiles_k, tiles;  // of columns, of x and of both; set by the launch
   float alpha;
 };
 int adapter_grad_piece(int64_t m, int64_t n, int64_t k);
 int64_t adapter_grad_slots(int64_t m, int piece);
 hipError_t launch_adapter_grad(const AdapterGradArgs &, int dtype, hipStream_t);
+// Both at once.
+hipError_t launch_adapter_both(const ExpandArgs &, const ExpandPlan &, const AdapterGradArgs &, int dtype,
+                               int dx_dtype, hipStream_t);
 
 // ----- dropout (adapter_kernels.hip) -------------------------------------------
 

@@ -125,7 +125,7 @@ def adapt(m=200, n=300, k=256, rank=16, count=5, x=A, ldx=256, sx=None, ldsx=0, 
 
 
 SIZES = [(dict(m=-1), EINVAL), (dict(n=-1), EINVAL), (dict(k=-1), EINVAL), (dict(rank=-1), EINVAL),
-         (dict(count=-1), EINVAL), (dict(m=(1 << 27) + 1), EINVAL), (dict(n=1 << 31), EINVAL), (dict(k=1 << 31), EINVAL),
+         (dict(count=-1), EINVAL), (dict(m=(1 << 26) + 1), EINVAL), (dict(n=1 << 31), EINVAL), (dict(k=1 << 31), EINVAL),
          (dict(rank=4097), EINVAL), (dict(count=65536), EINVAL), (dict(x=0), EINVAL), (dict(a=0), EINVAL),
          (dict(b=0), EINVAL), (dict(ids=0), EINVAL), (dict(ldx=255), EINVAL), (dict(lda=255), EINVAL),
          (dict(ldb=15), EINVAL), (dict(sa=-1), EINVAL), (dict(sb=-1), EINVAL), (dict(size=-1), EINVAL),
@@ -136,7 +136,6 @@ SIZES = [(dict(m=-1), EINVAL), (dict(n=-1), EINVAL), (dict(k=-1), EINVAL), (dict
 
 @pytest.mark.parametrize("args,want", SIZES + [
     (dict(out=0), EINVAL), (dict(ldout=299), EINVAL), (dict(ldbase=299), EINVAL),
-    (dict(m=1 << 27, n=1 << 20, ldout=1 << 20, ldbase=1 << 20, b=C, sb=0), EINVAL),
     (dict(sx=H, ldsx=199, ldx=256), EINVAL), (dict(sx=H, ldsx=200, ldx=260), EALIGN),
     (dict(sx=H, ldsx=200, x=A + 8), EALIGN), (dict(sx=H + 2, ldsx=200), EALIGN),
     (dict(out=F + 1), EALIGN), (dict(hidden=G + 2), EALIGN), (dict(out=A), EALIAS), (dict(out=B + 64), EALIAS),
@@ -175,7 +174,7 @@ def back(m=200, n=300, k=256, rank=16, count=5, dout=F, lddout=300, x=A, ldx=256
     (dict(dx=E + 2), EALIAS), (dict(dx=E, lddx=257), EALIAS), (dict(dx=A), EALIAS), (dict(dx=F), EALIAS),
     (dict(da=H), EALIAS), (dict(db=B), EALIAS), (dict(da=G), EALIAS), (dict(ws=H), EALIAS), (dict(ws=A), EALIAS),
     (dict(ws=0), EWORKSPACE), (dict(size=64), EWORKSPACE), (dict(ws=WS + 8), EALIGN),
-    (dict(m=1 << 27, n=1 << 20, k=1 << 20, ldx=1 << 20, lda=1 << 20, lddout=1 << 20, lddx=1 << 20, ldbase=1 << 20,
+    (dict(m=1 << 26, count=60000, n=1 << 20, k=1 << 20, ldx=1 << 20, lda=1 << 20, lddout=1 << 20, lddx=1 << 20, ldbase=1 << 20,
           dtype=F32, od=F32, size=1 << 62), EINVAL),
     (dict(dx=None, da=None, db=None), OK)])
 def test_adapters_backward_refusals(args, want):
@@ -192,6 +191,28 @@ def test_adapters_backward_workspace():
     assert ask(0, 0, 0, 0, 0, F32) == OK and size.value > 0
     assert ask(-1, 1, 1, 1, 1, F32) == EINVAL and ask(1, 1, 1, 1, 1, X.XPOSE_U8) == EDTYPE
     assert lib.xpose_adapters_backward_workspace(1, 1, 1, 1, 1, F32, None) == EINVAL
+
+
+def test_adapters_limits():
+    """The largest sizes are taken as far as their workspace, one more is refused before it."""
+    big = dict(x=A, a=B, b=C, ids=I, base=0, ws=0, hidden=None, sa=0, sb=0)
+    rows = dict(big, m=1 << 26, n=1, ldout=1, out=H + (1 << 39), a=A + (1 << 37), b=A + (1 << 38), k=1, ldx=1, lda=1)
+    assert adapt(**rows) == EWORKSPACE and adapt(**dict(rows, m=(1 << 26) + 1)) == EINVAL
+    wide = dict(m=2, n=1 << 30, k=1 << 30, ldx=1 << 30, lda=1 << 30, ldout=1 << 30, rank=1, ldb=1, x=1 << 44, a=2 << 44,
+                b=3 << 44, out=4 << 44, base=0, ws=0, hidden=None, sa=0, sb=0)
+    assert adapt(**wide) == EWORKSPACE
+    assert adapt(**dict(wide, n=(1 << 30) + 1, ldout=1 << 31)) == EINVAL
+    assert adapt(**dict(wide, k=(1 << 30) + 1, ldx=1 << 31, lda=1 << 31)) == EINVAL
+    size = ctypes.c_int64()
+    ask = lambda *v: lib.xpose_adapters_backward_workspace(*v, BF16, ctypes.byref(size))  # noqa: E731
+    tiles = 64  # of n and k together
+    most = ((1 << 23) - 768 - 1) // tiles - 1  # adapters next to fewer than 4096 rows
+    assert most > 65535 and ask(100, 4096, 4096, 16, 65535) == OK and ask(100, 4096, 4096, 16, 65536) == EINVAL
+    tiles = 512
+    most = ((1 << 23) - 768 - 1) // tiles - 1
+    assert ask(4095, 1 << 15, 1 << 15, 16, most) == OK and ask(4095, 1 << 15, 1 << 15, 16, most + 1) == EINVAL
+    assert ask(4096, 1 << 15, 1 << 15, 16, most) == EINVAL and ask(4096, 1 << 15, 1 << 15, 16, most - 1) == OK
+    assert ask(1 << 26, 1, 1, 4096, 65535) == OK and size.value > (1 << 38)
 
 
 # ----- dropout -----------------------------------------------------------------------
