@@ -116,7 +116,7 @@ int xpose_adapters_workspace(int64_t m, int64_t k, int64_t rank, int64_t count,
  * dense float32 of count x rank x k and count x n x rank, zeros for adapters of
  * no row.  dx, da and db may each be NULL: not wanted.  Sums are float32, in an
  * order of their own for each set of sizes and ids.  Limits as above, and
- * (m / 4096 + count + 1) (ceil(n / 128) + ceil(k / 128)) < 2^23 - 768. */
+ * (m / 4096 + count + 1) (ceil(n / 128) + ceil(k / 128)) < 2^23 - 256. */
 int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank,
                             int64_t count, const void *dout, int64_t lddout,
                             const void *x, int64_t ldx, const void *a,

@@ -840,8 +840,14 @@ __global__ __launch_bounds__(kExpandThreads) void expand_kernel(ExpandArgs a) {
 // ----- the adapters' gradients ----------------------------------------------------------
 //
 // G[r][c] = sum over rows u[row][r] v[row][c], u of r columns in float32, v as
-// it is: on the float32 matrix cores, whose operands need no turning around,
-// as a lane has one rank or eight neighbouring columns of one row in four.
+// it is.  With bfloat16 v, u is the sum of three bfloat16 numbers, as in `expand`;
+// a lane loads four columns of each of eight rows twice over and turns them around
+// in registers, a byte permutation for two values.  Other types take the float32
+// matrix cores, whose operands need no turning around, as a lane has one rank or
+// eight neighbouring columns of one row in four; in bfloat16 that took 8192 rows,
+// 4096 columns both ways, all gradients, with pieces of 1024 rows, 92 us for 84 at
+// rank 16, 137 for 97 at 32, 281 for 158 at 64.  (Float16 v would have to be split
+// too.)
 //
 // An adapter's rows are cut into pieces, a workgroup for 128 columns of each.
 // An adapter of one piece, or none, is done with that; the pieces of larger ones go to
@@ -857,14 +863,37 @@ constexpr int kGradThreads = 256, kGradCols = 128, kGradWaves = 4;
 
 __device__ inline int grad_pieces(int rows, int piece) { return (rows + piece - 1) / piece; }
 
+template <typename T> constexpr bool kGradSplit = std::is_same_v<T, __bf16>;
+template <typename T> constexpr int kGradRows = kGradSplit<T> ? 32 : 16;  // of a block
+
 template <typename T, int NR> struct GradRows {
   Vec8<T> v[4];
   float u[4][NR];
 };
+template <int NR> struct GradRows<__bf16, NR> {
+  u32x2 v[2][8];  // four columns of each half
+  float u[8][NR];
+};
+
+typedef u32x2 u32x2_by2 __attribute__((aligned(2)));
+// Four columns from `col` on, to be settled where they go past the end
+template <bool SHORT>
+__device__ inline u32x2 load_row4(const __bf16 *row, int64_t len, int64_t col) {
+  if constexpr (!SHORT) return *reinterpret_cast<const u32x2_by2 *>(row + (col < len - 4 ? col : len - 4));
+  __bf16 v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = col + e < len ? row[col + e] : (__bf16)0.f;
+  u32x2 w;
+  __builtin_memcpy(&w, v, 8);
+  return w;
+}
 
 template <typename T, int NR, bool SHORT>
 __device__ __forceinline__ void adapter_grad(const AdapterGradArgs &a, uint32_t block, f32x4 (*lds)[8][64]) {
-  constexpr int DEPTH = NR * (int)sizeof(T) <= 4 ? 3 : 2;  // blocks of rows under way, as registers allow
+  constexpr bool SPLIT = kGradSplit<T>;
+  // blocks of rows under way, as registers allow
+  constexpr int DEPTH = SPLIT ? (NR < 4 ? 2 : 1) : NR * (int)sizeof(T) <= 4 ? 3 : 2;
+  constexpr int BLOCK = kGradRows<T>;
   const int tiles_k = a.tiles_k, tiles = a.tiles;
   const int tid = threadIdx.x, lane = tid % 64, i16 = lane % 16, g = lane / 16;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
@@ -892,53 +921,106 @@ __device__ __forceinline__ void adapter_grad(const AdapterGradArgs &a, uint32_t 
   const int64_t ldv = of_b ? a.lddout : a.ldx;
   const float *u = of_b ? a.h : a.dh;
   const float factor = of_b ? a.alpha * (a.scale ? a.scale[l] : 1.f) : 1.f;
-  const int64_t col = c0 + 8 * i16;
+  const int64_t col = c0 + (SPLIT ? 4 : 8) * i16;  // SPLIT: and 64 on
 
   f32x4 sum[NR][8];
 #pragma unroll
   for (int q = 0; q < NR; ++q)
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[q][e] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // 16 rows at a time, the next ones' loads under way and the numbers of those
+  // BLOCK rows at a time, the next ones' loads under way and the numbers of those
   // after them; past the end the last row is read, for nothing
   GradRows<T, NR> rows_of[DEPTH];
   int numbers[DEPTH];
-  auto number_of = [&](int p0) { return a.order[min(p0 + i16, end - 1)]; };
+  auto number_of = [&](int p0) { return a.order[min(p0 + lane % BLOCK, end - 1)]; };
   // rows with these numbers; then numbers are those of p0
   auto load = [&](int &numbers, int p0, GradRows<T, NR> &to) {
-    int64_t row[4];
+    int64_t row[BLOCK / 4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) row[s] = __shfl(numbers, 4 * s + g);
+    for (int s = 0; s < BLOCK / 4; ++s) row[s] = __shfl(numbers, SPLIT ? 8 * g + s : 4 * s + g);
     __builtin_amdgcn_sched_barrier(0);
     numbers = number_of(p0);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < BLOCK / 4; ++s) {
       const T *from = v + row[s] * ldv;
-      if constexpr (SHORT) to.v[s] = load_raw8(from + col, valid8(cols - col));
-      else to.v[s] = load_row8(from, cols, col);
+      if constexpr (SPLIT) {
+        to.v[0][s] = load_row4<SHORT>(from, cols, col);
+        to.v[1][s] = load_row4<SHORT>(from, cols, col + 64);
+      } else if constexpr (SHORT) {
+        to.v[s] = load_raw8(from + col, valid8(cols - col));
+      } else {
+        to.v[s] = load_row8(from, cols, col);
+      }
 #pragma unroll
       for (int q = 0; q < NR; ++q) to.u[s][q] = u[row[s] * a.rank + min(r0 + 16 * q + i16, a.rank - 1)];
     }
     __builtin_amdgcn_sched_barrier(0);
   };
   auto multiply = [&](int p0, GradRows<T, NR> &rows) {
+    if constexpr (SPLIT) {
+      if (!SHORT && c0 + kGradCols > cols)
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const bool in = p0 + 4 * s + g < end;  // rows past the piece may hold anything
-      if constexpr (!SHORT) settle8<T>(rows.v[s], cols, col);
+        for (int h = 0; h < 2; ++h) {
+          const int64_t past = col + 64 * h + 4 - cols;
+          const int by = past < 0 ? 0 : past < 4 ? (int)past : 4;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float f = in ? at8<T>(rows.v[s], e) : 0.f;
+          for (int s = 0; s < 8; ++s) {
+            uint64_t w = (uint64_t)rows.v[h][s][1] << 32 | rows.v[h][s][0];
+            w = by < 4 ? w >> (16 * by) : 0;
+            rows.v[h][s] = u32x2{(uint32_t)w, (uint32_t)(w >> 32)};
+          }
+        }
+      if (p0 + BLOCK > end)  // rows past the piece may hold anything
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          const bool in = p0 + 8 * g + s < end;
+#pragma unroll
+          for (int q = 0; q < NR; ++q) rows.u[s][q] = in ? rows.u[s][q] : 0.f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) rows.v[h][s][i] = in ? rows.v[h][s][i] : 0;
+        }
+      Split8<T> part[NR];
+#pragma unroll
+      for (int q = 0; q < NR; ++q) {
+        float f[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) f[s] = rows.u[s][q];
+        part[q].set(f);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {  // a column: its rows two by two
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = __builtin_amdgcn_perm(rows.v[e / 4][2 * i + 1][e % 4 / 2], rows.v[e / 4][2 * i][e % 4 / 2],
+                                       e % 2 ? 0x07060302u : 0x05040100u);
 #pragma unroll
         for (int q = 0; q < NR; ++q)
-          sum[q][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(in ? rows.u[s][q] : 0.f, f, sum[q][e], 0, 0, 0);
+#pragma unroll
+          for (int p = 2; p >= 0; --p)
+            sum[q][e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part[q].part[p], __builtin_bit_cast(bf16x8, w), sum[q][e], 0, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const bool in = p0 + 4 * s + g < end;  // rows past the piece may hold anything
+        if constexpr (!SHORT) settle8<T>(rows.v[s], cols, col);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float f = in ? at8<T>(rows.v[s], e) : 0.f;
+#pragma unroll
+          for (int q = 0; q < NR; ++q)
+            sum[q][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(in ? rows.u[s][q] : 0.f, f, sum[q][e], 0, 0, 0);
+        }
       }
     }
   };
   // as in shrink_kernel, one way through the loop
-  constexpr int kApart = 16 * kGradWaves;
-  const int start_at = begin + 16 * wave;
+  constexpr int kApart = BLOCK * kGradWaves;
+  const int start_at = begin + BLOCK * wave;
   if (start_at < end) {
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) numbers[d] = number_of(start_at + d * kApart);
@@ -962,10 +1044,12 @@ __device__ __forceinline__ void adapter_grad(const AdapterGradArgs &a, uint32_t 
     }
     __syncthreads();
   }
-  // lds[q][e][lane] has columns 8 (lane % 16) + e, ranks 16 q + 4 (lane / 16) and on
+  // lds[q][e][lane] has ranks 16 q + 4 (lane / 16) and on of column 8 (lane % 16) + e,
+  // or 64 (e / 4) + 4 (lane % 16) + e % 4
   const float *flat = (const float *)lds;
   auto value = [&](int r, int c) {
-    return flat[(((r / 16) * 8 + c % 8) * 64 + r % 16 / 4 * 16 + c / 8) * 4 + r % 4] * factor;
+    const int e = SPLIT ? c / 64 * 4 + c % 4 : c % 8, of = SPLIT ? c % 64 / 4 : c / 8;
+    return flat[(((r / 16) * 8 + e) * 64 + r % 16 / 4 * 16 + of) * 4 + r % 4] * factor;
   };
   const int ranks = min(a.rank - r0, 16 * NR), here = (int)min(cols - c0, (int64_t)kGradCols);
   const int64_t slot = 2 * (int64_t)(start / a.piece) + j, each = (int64_t)a.rank * (a.k + a.n);
@@ -991,8 +1075,10 @@ __global__ __launch_bounds__(kGradThreads) void adapter_grad_kernel(AdapterGradA
 
 // dx and the adapters' gradients in one launch, which need nothing of each other,
 // a workgroup of each in turn: 8192 rows, 4096 columns both ways, bfloat16 take
-// 92 us a pass, 96 with one after the other and 98 in two launches, 300 rows 23
-// and 28.
+// 81 us a pass, some 5 more one after the other or in two launches, 300 rows 20 and
+// 25.  For over 32 ranks they are two launches: more sums than let two workgroups
+// of both kinds share a compute unit (rank 64, pieces of 1024 rows, 158 us, 171 and
+// 242 here with 32 and 64 ranks a workgroup, float32 2048 rows 98 and 119).
 template <typename T, typename O, int NR, bool SHORT>
 __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NR < 4 ? 2 : 1) void adapter_both_kernel(ExpandArgs e, AdapterGradArgs g, uint32_t expands) {
   constexpr int kBytes = kExpandLds<T, 4> > NR * 8192 ? kExpandLds<T, 4> : NR * 8192;
@@ -1154,11 +1240,11 @@ struct GradGrid {
   int nr;
   bool narrow;  // columns shorter than a load
 };
-GradGrid grad_grid(AdapterGradArgs &a) {
+GradGrid grad_grid(AdapterGradArgs &a, bool wide) {
   a.tiles_k = a.da ? (int)((a.k + kGradCols - 1) / kGradCols) : 0;
   a.tiles = a.tiles_k + (a.db ? (int)((a.n + kGradCols - 1) / kGradCols) : 0);
   GradGrid g{};
-  g.nr = a.rank <= 16 ? 1 : a.rank <= 32 ? 2 : 4;
+  g.nr = a.rank <= 16 ? 1 : a.rank <= 32 || !wide ? 2 : 4;
   g.groups = (uint32_t)((a.m / a.piece + a.count) * a.tiles);
   g.chunks = (uint32_t)((a.rank + 16 * g.nr - 1) / (16 * g.nr));
   g.narrow = (a.da && a.k < 8) || (a.db && a.n < 8);
@@ -1173,14 +1259,15 @@ hipError_t grad_sum(const AdapterGradArgs &a, hipStream_t s) {
 }
 template <typename T, bool SHORT>
 hipError_t grad(const AdapterGradArgs &a, const GradGrid &g, hipStream_t s) {
+  constexpr int most = kGradSplit<T> ? 4 : 2;
   const void *kernel = g.nr == 1   ? reinterpret_cast<const void *>(&adapter_grad_kernel<T, 1, SHORT>)
                        : g.nr == 2 ? reinterpret_cast<const void *>(&adapter_grad_kernel<T, 2, SHORT>)
-                                   : reinterpret_cast<const void *>(&adapter_grad_kernel<T, 4, SHORT>);
+                                   : reinterpret_cast<const void *>(&adapter_grad_kernel<T, most, SHORT>);
   return launch(kernel, dim3(g.groups, g.chunks), kGradThreads, s, a);
 }
 template <typename T>
 hipError_t grad(AdapterGradArgs a, hipStream_t s) {
-  const GradGrid g = grad_grid(a);
+  const GradGrid g = grad_grid(a, kGradSplit<T>);
   if (g.groups == 0) return hipSuccess;
   const hipError_t e = g.narrow ? grad<T, true>(a, g, s) : grad<T, false>(a, g, s);
   return e == hipSuccess ? grad_sum(a, s) : e;
@@ -1195,13 +1282,11 @@ hipError_t both(ExpandArgs e, const ExpandPlan &p, const AdapterGradArgs &a, con
 }
 template <typename T, typename O, bool SHORT>
 hipError_t both(const ExpandArgs &e, const ExpandPlan &p, const AdapterGradArgs &a, const GradGrid &g, hipStream_t s) {
-  return g.nr == 1   ? both<T, O, 1, SHORT>(e, p, a, g, s)
-         : g.nr == 2 ? both<T, O, 2, SHORT>(e, p, a, g, s)
-                     : both<T, O, 4, SHORT>(e, p, a, g, s);
+  return g.nr == 1 ? both<T, O, 1, SHORT>(e, p, a, g, s) : both<T, O, 2, SHORT>(e, p, a, g, s);
 }
 template <typename T, typename O>
 hipError_t both(const ExpandArgs &e, const ExpandPlan &p, AdapterGradArgs a, hipStream_t s) {
-  const GradGrid g = grad_grid(a);
+  const GradGrid g = grad_grid(a, false);
   const hipError_t err = g.narrow || e.n < 8 || e.rank < 8 ? both<T, O, true>(e, p, a, g, s) : both<T, O, false>(e, p, a, g, s);
   return err == hipSuccess ? grad_sum(a, s) : err;
 }
@@ -1255,10 +1340,11 @@ hipError_t launch_expand(const ExpandArgs &a, const ExpandPlan &p, int dtype, in
 int adapter_grad_piece(int64_t m, int64_t n, int64_t k) {
   const int64_t tiles = (n + kGradCols - 1) / kGradCols + (k + kGradCols - 1) / kGradCols;
   if (m <= 512) return 512;  // one piece an adapter: no second launch (300 rows 28 and 23 us a pass)
-  // three workgroups a compute unit or fewer (8192 rows, 4096 columns both ways: 128
-  // rows a piece 128 us, 256 111, 512 104, 1024 101, 2048 117)
+  // a workgroup a compute unit, next to the other kernel's (8192 rows, 4096 columns
+  // both ways, bfloat16: 128 rows a piece 130 us, 256 101, 512 92, 1024 85, 2048 82,
+  // 4096 83; 2048 rows in float32: 128 55 us, 512 45, 2048 44)
   int piece = 128;
-  while (piece < 4096 && m / piece * tiles > 768) piece *= 2;
+  while (piece < 4096 && m / piece * tiles > 256) piece *= 2;
   return piece;
 }
 int64_t adapter_grad_slots(int64_t m, int piece) { return m > piece ? 2 * (m / piece + 1) : 0; }

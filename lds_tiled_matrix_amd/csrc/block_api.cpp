@@ -284,8 +284,8 @@ struct BackwardParts {
   int piece;
 };
 bool backward_parts(int64_t m, int64_t n, int64_t k, int64_t rank, int64_t count, int size, BackwardParts &w) {
-  // pieces of 4096 rows, or shorter ones, 768 workgroups at most
-  if ((m / 4096 + count + 1) * (ceil_div(n, 128) + ceil_div(k, 128)) >= kMaxGradGroups - 768) return false;
+  // pieces of 4096 rows, or shorter ones, 256 workgroups at most
+  if ((m / 4096 + count + 1) * (ceil_div(n, 128) + ceil_div(k, 128)) >= kMaxGradGroups - 256) return false;
   Parts p;
   w.plan = xpose::shrink_plan(std::max<int64_t>(m, 1), n, rank, count, size, true);
   w.piece = xpose::adapter_grad_piece(m, n, k);
@@ -373,7 +373,7 @@ int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank, int64
     if (rc != XPOSE_OK) return rc;
   }
   const int64_t used = some ? count : 0;
-  const bool beside = copies && weights;
+  const bool beside = copies && weights && rank <= 32;
   const xpose::ExpandPlan plan = xpose::expand_plan(m, k, used, beside);
   xpose::ExpandArgs e{};
   e.h = dh;
@@ -395,7 +395,10 @@ int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank, int64
   e.slots = plan.slots;
   e.strips = (int32_t)plan.strips;
   e.alpha = 1.f;
-  if (!weights) return hip(xpose::launch_expand(e, plan, dtype, dx_dtype, (hipStream_t)stream));
+  if (copies && !beside) {
+    rc = hip(xpose::launch_expand(e, plan, dtype, dx_dtype, (hipStream_t)stream));
+    if (rc != XPOSE_OK || !weights) return rc;
+  }
   xpose::AdapterGradArgs g{};
   g.dh = dh;
   g.h = hidden;

@@ -206,10 +206,10 @@ def test_adapters_limits():
     size = ctypes.c_int64()
     ask = lambda *v: lib.xpose_adapters_backward_workspace(*v, BF16, ctypes.byref(size))  # noqa: E731
     tiles = 64  # of n and k together
-    most = ((1 << 23) - 768 - 1) // tiles - 1  # adapters next to fewer than 4096 rows
+    most = ((1 << 23) - 256 - 1) // tiles - 1  # adapters next to fewer than 4096 rows
     assert most > 65535 and ask(100, 4096, 4096, 16, 65535) == OK and ask(100, 4096, 4096, 16, 65536) == EINVAL
     tiles = 512
-    most = ((1 << 23) - 768 - 1) // tiles - 1
+    most = ((1 << 23) - 256 - 1) // tiles - 1
     assert ask(4095, 1 << 15, 1 << 15, 16, most) == OK and ask(4095, 1 << 15, 1 << 15, 16, most + 1) == EINVAL
     assert ask(4096, 1 << 15, 1 << 15, 16, most) == EINVAL and ask(4096, 1 << 15, 1 << 15, 16, most - 1) == OK
     assert ask(1 << 26, 1, 1, 4096, 65535) == OK and size.value > (1 << 38)
