@@ -436,7 +436,7 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(ShrinkArgs a) {
       return to;
     };
     auto multiply = [&](Step &v) {
-      if constexpr (WT && !SHORT)
+      if constexpr (WT && !SHORT && NR < 4)  // four are for whole chunks of ranks alone
 #pragma unroll
         for (int q = 0; q < NR; ++q)
 #pragma unroll
@@ -1170,13 +1170,14 @@ hipError_t shrink(const ShrinkArgs &a, const ShrinkPlan &p, hipStream_t s) {
 }
 template <typename T, bool Q, int NI, bool WT>
 hipError_t shrink_rank(const ShrinkArgs &a, const ShrinkPlan &p, hipStream_t s) {
-  // weights take 16 registers a rank and step, twice that next to e4m3, four
-  // times in float32 next to e4m3: more would spill
-  constexpr int most = Q ? (sizeof(T) == 2 && NI == 1 ? 2 : 1) : sizeof(T) == 2 && !WT ? 4 : 2;
+  // weights take 8 registers for 16 ranks and a step, twice that next to e4m3, four
+  // times in float32 next to e4m3: more would spill.  So would 64 turned ranks that
+  // end inside a chunk; whole ones take 27 us for 8192 x 4096, 47 as twice 32.
+  constexpr int most = Q ? (sizeof(T) == 2 && NI == 1 ? 2 : 1) : sizeof(T) == 2 ? 4 : 2;
   if constexpr (WT)
     if (a.rank < kChunk<T>) return shrink<T, Q, NI, 1, WT, true>(a, p, s);
   if (a.rank <= 16 || most == 1) return shrink<T, Q, NI, 1, WT, false>(a, p, s);
-  return a.rank <= 32 || most == 2 ? shrink<T, Q, NI, most < 2 ? 1 : 2, WT, false>(a, p, s)
+  return a.rank <= 32 || most == 2 || (WT && a.rank % 8) ? shrink<T, Q, NI, most < 2 ? 1 : 2, WT, false>(a, p, s)
                                    : shrink<T, Q, NI, most, WT, false>(a, p, s);
 }
 template <typename T, bool Q, bool WT>

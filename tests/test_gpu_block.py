@@ -336,7 +336,8 @@ def _check_adapters(c, pads=(0, 3)):
 
 ADAPTER_SIZES = [(1, 1, 1, 1, 1), (1, 300, 128, 16, 3), (2, 17, 1000, 8, 1), (5, 64, 257, 4, 2), (16, 257, 130, 16, 9),
                  (17, 40, 3, 5, 4), (31, 256, 4100, 12, 40), (64, 333, 640, 16, 64), (65, 513, 127, 24, 3),
-                 (100, 100, 300, 32, 2), (150, 70, 1222, 64, 5), (33, 90, 200, 100, 3), (7, 5, 7, 2, 3)]
+                 (100, 100, 300, 32, 2), (150, 70, 1222, 64, 5), (33, 90, 200, 100, 3), (7, 5, 7, 2, 3),
+                 (90, 130, 1500, 72, 3), (40, 1100, 6, 128, 2), (70, 6, 515, 33, 4)]
 
 
 @pytest.mark.parametrize("m,n,k,rank,count", ADAPTER_SIZES)
