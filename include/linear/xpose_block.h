@@ -115,7 +115,8 @@ int xpose_adapters_workspace(int64_t m, int64_t k, int64_t rank, int64_t count,
  * dx_dtype, dtype or XPOSE_F32; dx may be base itself (same pitch).  da and db:
  * dense float32 of count x rank x k and count x n x rank, zeros for adapters of
  * no row.  dx, da and db may each be NULL: not wanted.  Sums are float32, in an
- * order of their own for each set of sizes and ids.  Limits as above, and
+ * order of their own for each set of sizes and ids; where a term holds an
+ * infinity, its sum is infinite or NaN.  Limits as above, and
  * (m / 4096 + count + 1) (ceil(n / 128) + ceil(k / 128)) < 2^23 - 256. */
 int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank,
                             int64_t count, const void *dout, int64_t lddout,

@@ -12,6 +12,7 @@ as ``out`` or ``residual_out`` counts as a change in place.
 from __future__ import annotations
 
 import ctypes
+import operator
 
 from .linear import _lib, _torch_side
 
@@ -124,6 +125,6 @@ def dropout(x, p: float, seed, *, offset: int = 0, residual=None, out=None, stre
     graphs whose replays are to differ.  ``offset`` tells the dropouts of one
     seed apart; both count modulo 2^64.  p counts in steps of 2^-16.  ``out``
     may be x or residual."""
-    if isinstance(seed, int):
-        seed &= (1 << 64) - 1
-    return _torch_side().dropout(x, p, seed, offset & ((1 << 64) - 1), residual, out, stream)
+    if hasattr(seed, "__index__") and not hasattr(seed, "data_ptr"):
+        seed = operator.index(seed) & ((1 << 64) - 1)
+    return _torch_side().dropout(x, p, seed, operator.index(offset) & ((1 << 64) - 1), residual, out, stream)

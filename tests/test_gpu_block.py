@@ -646,6 +646,8 @@ def test_dropout_masks_differ_and_are_the_gradients():
         for q in masks[:i]:
             assert abs((p & q).sum().item() - 0.5625 * n) < 6 * (n * 0.5625 * 0.4375) ** 0.5
     assert torch.equal(X.dropout(x, 0.25, (1 << 64) + 1) != 0, masks[0])
+    assert torch.equal(X.dropout(x, 0.25, np.int64(1), offset=np.uint8(1)) != 0, masks[2])
+    assert torch.equal(X.dropout(x, 0.25, np.int64(-1)), X.dropout(x, 0.25, torch.tensor([-1], device=_dev())))
     assert torch.equal(X.dropout(x[:, :501], 0.25, 1) != 0, masks[0][:, :501])
     assert torch.equal(X.dropout(x.bfloat16()[:77], 0.25, 1) != 0, masks[0][:77])
     dy = torch.randn_like(x)
