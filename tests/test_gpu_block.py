@@ -359,6 +359,14 @@ def test_adapters_of_many_rows(m, k, quantized, kind):
     _check_adapters(_adapter_case(m, 300, k, 16, 5, BF16, BF16, m, quantized, ids), pads=(0,))
 
 
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("rank", [5, 16, 40])
+def test_adapters_of_many_e4m3_rows(dtype, rank):
+    say(f"adapters e4m3 rows {dtype} {rank}")
+    ids = np.arange(4500) * 7 // 300 % 6 - 1
+    _check_adapters(_adapter_case(4500, 130, 333, rank, 4, dtype, dtype, rank, True, ids), pads=(0,))
+
+
 def test_adapters_slices_and_slots():
     """One token with a long k; rows with an adapter each and all the same."""
     _check_adapters(_adapter_case(1, 100, 8200, 16, 4, BF16, F32, 1, ids=[2]))
@@ -523,6 +531,35 @@ def test_adapters_backward_rows(m, kind):
     _check_backward(c, pads=(0,))
     first = _run_backward(c)
     assert all(torch.equal(p, q) for p, q in zip(first, _run_backward(c)))
+
+
+@pytest.mark.parametrize("rank", [3, 24, 40, 64, 65, 136])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_adapters_backward_ranks(rank, dtype):
+    """Ranks in one, two and more workgroups, of several pieces each."""
+    ids = np.arange(1500) * 9 // 1500 % 4 - 1
+    say(f"adapters_backward ranks {rank} {dtype}")
+    c = _backward_case(1500, 190, 260, rank, 3, dtype, dtype, rank, ids)
+    _check_backward(c, pads=(0, 3))
+    whole = _run_backward(c)
+    for wanted in ((1, 0, 0), (0, 1, 1)):
+        got = _run_backward(c, wanted=wanted, **({} if wanted[0] else {"base": None}))
+        assert all(g is None or torch.equal(g, v) for g, v in zip(got, whole))
+
+
+def test_adapters_backward_infinities():
+    """An infinity among what is summed reaches its own sums and no others."""
+    for dtype in TYPES:
+        c = _backward_case(150, 100, 140, 16, 2, dtype, dtype, 5, ids=np.arange(150) % 3)
+        clean = [t.cpu() for t in _run_backward(c)]
+        c["x"][33, 7], c["hidden"][36, 2], c["dout"][39, 5] = math.inf, -math.inf, math.inf
+        got = [t.cpu() for t in _run_backward(c)]
+        rows, ranks, cols = torch.arange(150) != 39, torch.arange(16) != 2, torch.arange(100) != 5
+        assert torch.equal(got[0][rows], clean[0][rows]) and not got[0][39].isfinite().any()
+        assert torch.equal(got[1][1], clean[1][1]) and torch.equal(got[2][1], clean[2][1])
+        assert not got[1][0].isfinite().any()  # dh of row 39 is not finite
+        assert torch.equal(got[2][0][cols][:, ranks], clean[2][0][cols][:, ranks])
+        assert not got[2][0][5].isfinite().any() and not got[2][0][:, 2].isfinite().any()
 
 
 def test_adapters_backward_large_pieces():

@@ -310,6 +310,33 @@ def test_a_step_in_a_graph(m):
             eager[0].mul_(0.5)
 
 
+def test_a_graph_of_other_sizes_than_were_called_before():
+    """Nothing has to be called eagerly first: sizes, types and kernels that only
+    the capture uses."""
+    gen = torch.Generator(device=_dev()).manual_seed(2)
+    r = lambda *s: torch.randn(*s, generator=gen, device=_dev())  # noqa: E731
+    x, a, b = r(77, 96).half(), r(3, 24, 96).half(), r(3, 112, 24).half()
+    ids = (torch.arange(77, device=_dev()) % 4).int()
+
+    def run():
+        y, rstd = X.rms_norm(x, stats=True)
+        out, hidden = X.adapters(y, a, b, ids, hidden=True)
+        dropped = X.dropout(out, 0.5, 3)
+        dy, da, db = X.adapters_backward(dropped, y, a, b, ids, hidden)
+        return [out, dropped, dy, da, db, *X.rms_norm_backward(dy, x, rstd)]
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for turn in range(3):
+        x.mul_(0.9)
+        graph.replay()
+        want = run()
+        torch.cuda.synchronize()
+        assert _same(got, want)
+
+
 # ----- places ---------------------------------------------------------------------------
 
 def _far(t, pitch):
