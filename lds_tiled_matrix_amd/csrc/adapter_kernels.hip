@@ -1223,7 +1223,7 @@ hipError_t expand(ExpandArgs a, const ExpandPlan &p, hipStream_t s) {
 }
 template <typename T, typename O, bool WT, bool SHORT>
 hipError_t expand(const ExpandArgs &a, const ExpandPlan &p, hipStream_t s) {
-  return p.waves_down == 4 ? expand<T, O, 4, WT, SHORT>(a, p, s) : expand<T, O, 1, WT, SHORT>(a, p, s);
+  return p.waves_down == 4 ? expand<T, O, 4, WT, SHORT>(a, p, s) : expand<T, O, 2, WT, SHORT>(a, p, s);
 }
 template <typename T, typename O, bool WT>
 hipError_t expand(const ExpandArgs &a, const ExpandPlan &p, hipStream_t s) {
@@ -1321,7 +1321,10 @@ hipError_t launch_shrink(const ShrinkArgs &a, const ShrinkPlan &p, int dtype, hi
 
 ExpandPlan expand_plan(int64_t m, int64_t n, int64_t count, bool beside) {
   ExpandPlan p{};
-  p.waves_down = m > 16 || beside ? 4 : 1;
+  // Few rows leave waves down without any, but share h among fewer workgroups: 16
+  // tokens beside e4m3 10.6 us a call with 2, 11.1 with 1 and 11.3 with 4, 64 rows 9.3,
+  // 9.8 and 9.1 (4096 columns both ways).
+  p.waves_down = m > 16 || beside ? 4 : 2;
   const int rows = 16 * p.waves_down, cols = kExpandCols * kExpandWaves / p.waves_down;
   p.strips = (n + cols - 1) / cols;
   p.tiles = (m + rows - 1) / rows;
