@@ -82,8 +82,8 @@ int xpose_rms_norm_backward_workspace(int64_t rows, int64_t cols,
  * of rank x k, row pitch lda, stride_a from one to the next; b: of n x rank,
  * ldb, stride_b; both of dtype.  scale (NULL: ones): count float32 values.
  * base (NULL: zeros) and out: m x n of out_dtype, which is dtype or XPOSE_F32;
- * out may be base itself (same pitch).  hidden (NULL: not wanted): m x rank
- * float32 values, dense.  ids: m values.
+ * out may be base itself (same pitch), and base x.  hidden (NULL: not wanted):
+ * m x rank float32 values, dense.  ids: m values.
  *
  * hidden is summed in float32 and stays float32; out is formed in float32 and
  * rounded once.  Where hidden or B holds an infinity, what it goes into is
@@ -112,11 +112,12 @@ int xpose_adapters_workspace(int64_t m, int64_t k, int64_t rank, int64_t count,
  *
  * x and dout are of dtype (x is the forward call's, or what it was quantised
  * from), hidden is the forward call's.  base (NULL: zeros) and dx: m x k of
- * dx_dtype, dtype or XPOSE_F32; dx may be base itself (same pitch).  da and db:
- * dense float32 of count x rank x k and count x n x rank, zeros for adapters of
- * no row.  dx, da and db may each be NULL: not wanted.  Sums are float32, in an
- * order of their own for each set of sizes and ids; where a term holds an
- * infinity, its sum is infinite or NaN.  Limits as above, and
+ * dx_dtype, dtype or XPOSE_F32; dx may be base itself (same pitch), and base
+ * dout or x: the gradients are then formed before dx.  da and db: dense float32
+ * of count x rank x k and count x n x rank, zeros for adapters of no row.  dx,
+ * da and db may each be NULL: not wanted.  Sums are float32, in an order of
+ * their own for each set of sizes and ids; where a term holds an infinity, its
+ * sum is infinite or NaN.  Limits as above, and
  * (m / 4096 + count + 1) (ceil(n / 128) + ceil(k / 128)) < 2^23 - 256. */
 int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank,
                             int64_t count, const void *dout, int64_t lddout,

@@ -95,7 +95,8 @@ def adapters(x, a, b, ids, *, base=None, scale=1.0, scale_x=None, hidden: bool =
     bfloat16; ``ids``: m values of int32, in any order; ``base`` (None: zeros):
     (m, n) of the adapters' dtype or float32, which the result has too;
     ``scale``: a number, or a float32 tensor of one for each adapter.  ``out``
-    may be base itself; rows without an adapter are left as they are then.
+    may be base itself (x where that is base); rows without an adapter are left
+    as they are then.
     With ``hidden`` (out, hidden), the latter x A.T in float32, which
     ``adapters_backward`` needs."""
     got = _torch_side().adapters(x, a, b, ids, base, scale, scale_x, hidden, out, stream)
@@ -107,9 +108,9 @@ def adapters_backward(dout, x, a, b, ids, hidden, *, base=None, scale=1.0, wante
     """(dx, da, db) for the gradient dout of ``adapters(x, a, b, ids,
     hidden=True)``.  ``base`` (None: zeros) is what dx is added to, such as the
     shared product's gradient of x, and sets its dtype; ``out``, where dx goes,
-    may be base itself.  da and db are float32, shaped as a and b, zeros for
-    adapters of no row.  ``wanted`` says which of the three are: the others are
-    None and cost nothing."""
+    may be base itself (dout or x where that is base).  da and db are float32,
+    shaped as a and b, zeros for adapters of no row.  ``wanted`` says which of
+    the three are: the others are None and cost nothing."""
     return tuple(_torch_side().adapters_backward(dout, x, a, b, ids, hidden, base, scale, list(wanted), out, stream))
 
 

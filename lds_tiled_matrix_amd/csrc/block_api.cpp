@@ -57,20 +57,21 @@ static int rms_norm(int64_t rows, int64_t cols, const void *x, int64_t ldx, int3
   const int size = size_of(dtype), param = size_of(param_dtype);
   if (!size || !param) return XPOSE_EDTYPE;
   Ranges r;
-  r.matrix(x, rows, cols, ldx, size, size, false);
+  const int in = r.matrix(x, rows, cols, ldx, size, size, false);
+  int res = -1;
   if (residual) {
-    r.matrix(residual, rows, cols, ldr, size, size, false);
-    r.matrix(h, rows, cols, ldh, size, size, true);
-    r.same(x, h);
-    r.same(residual, h);
+    res = r.matrix(residual, rows, cols, ldr, size, size, false);
+    const int sum = r.matrix(h, rows, cols, ldh, size, size, true);
+    r.same(in, sum);
+    r.same(res, sum);
   }
   if (weight) r.vector(weight, cols, param, false);
-  r.matrix(y, rows, cols, ldy, quantized ? 1 : size, quantized ? 8 : size, true);
+  const int out = r.matrix(y, rows, cols, ldy, quantized ? 1 : size, quantized ? 8 : size, true);
   if (quantized) {
     r.matrix(scale, ceil_div(cols, kBlock), rows, ld_scale, 4, 4, true);
   } else {
-    r.same(x, y);
-    r.same(residual, y);
+    r.same(in, out);
+    r.same(res, out);
   }
   if (rstd && cols) r.vector(rstd, rows, 4, true);
   const int rc = r.check();
@@ -143,14 +144,15 @@ int xpose_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t 
   if (rc != XPOSE_OK) return rc;
   if (!xpose::rms_norm_bwd_fits(rows, cols)) return XPOSE_EINVAL;
   Ranges r;
-  r.matrix(dy, rows, cols, lddy, size, size, false);
-  r.matrix(h, rows, cols, ldh, size, size, false);
-  if (dresidual) r.matrix(dresidual, rows, cols, ld_dresidual, size, size, false);
+  const int in = r.matrix(dy, rows, cols, lddy, size, size, false);
+  const int in_h = r.matrix(h, rows, cols, ldh, size, size, false);
+  const int res = dresidual ? r.matrix(dresidual, rows, cols, ld_dresidual, size, size, false) : -1;
   if (cols) r.vector(rstd, rows, 4, false);
   if (weight) r.vector(weight, cols, param, false);
-  r.matrix(dx, rows, cols, lddx, size, size, true);
-  r.same(dy, dx);
-  r.same(dresidual, dx);
+  const int out = r.matrix(dx, rows, cols, lddx, size, size, true);
+  r.same(in, out);
+  r.same(res, out);
+  if (dx == dy || dx == dresidual) r.same(in_h, out);  // h may be either: all are read before dx is written there
   if (dweight) r.vector(dweight, cols, 4, true);
   const bool enough = workspace && workspace_bytes / 4 >= floats;
   if (enough && floats) r.matrix(workspace, 1, floats, floats, 4, 4, true);
@@ -209,15 +211,16 @@ int xpose_adapters(int64_t m, int64_t n, int64_t k, int64_t rank, int64_t count,
   if (rc != XPOSE_OK) return rc;
   const bool some = m && rank && count;  // whether anything of A and x is read
   Ranges r;
-  r.matrix(x, some ? m : 0, k, ldx, x_size, scale_x ? 16 : size, false);
+  const int in = r.matrix(x, some ? m : 0, k, ldx, x_size, scale_x ? 16 : size, false);
   if (scale_x) r.matrix(scale_x, some ? ceil_div(k, kBlock) : 0, m, ld_scale_x, 4, 4, false);
   r.matrices(a, some ? count : 0, stride_a, rank, k, lda, size);
   r.matrices(b, some ? count : 0, stride_b, n, rank, ldb, size);
   r.vector(ids, m, 4, false);
   if (scale) r.vector(scale, count, 4, false);
-  if (base) r.matrix(base, m, n, ld_base, out_size, out_size, false);
-  r.matrix(out, m, n, ld_out, out_size, out_size, true);
-  r.same(base, out);
+  const int from = base ? r.matrix(base, m, n, ld_base, out_size, out_size, false) : -1;
+  const int to = r.matrix(out, m, n, ld_out, out_size, out_size, true);
+  r.same(from, to);
+  if (base == out) r.same(in, to);  // base may be x, which only the first launch reads
   if (hidden) r.vector(hidden, m * rank, 4, true);
   const bool enough = need == 0 || (workspace && workspace_bytes >= need);
   if (need && enough) r.matrix(workspace, 1, need, need, 1, 16, true);
@@ -322,17 +325,21 @@ int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank, int64
   if (!backward_parts(m, n, k, rank, count, size, w)) return XPOSE_EINVAL;
   const bool some = m && rank && count;
   Ranges r;
-  r.matrix(dout, some ? m : 0, n, lddout, size, size, false);
-  if (da) r.matrix(x, some ? m : 0, k, ldx, size, size, false);
+  const int in_dout = r.matrix(dout, some ? m : 0, n, lddout, size, size, false);
+  const int in_x = da ? r.matrix(x, some ? m : 0, k, ldx, size, size, false) : -1;
   if (dx) r.matrices(a, some ? count : 0, stride_a, rank, k, lda, size);
   if (dx || da) r.matrices(b, some ? count : 0, stride_b, n, rank, ldb, size);
   r.vector(ids, m, 4, false);
   if (scale) r.vector(scale, count, 4, false);
   if (db) r.vector(hidden, some ? m * rank : 0, 4, false);
   if (dx) {
-    if (base) r.matrix(base, m, k, ld_base, dx_size, dx_size, false);
-    r.matrix(dx, m, k, lddx, dx_size, dx_size, true);
-    r.same(base, dx);
+    const int from = base ? r.matrix(base, m, k, ld_base, dx_size, dx_size, false) : -1;
+    const int to = r.matrix(dx, m, k, lddx, dx_size, dx_size, true);
+    r.same(from, to);
+    if (base == dx) {  // base may be dout or x
+      r.same(in_dout, to);
+      r.same(in_x, to);
+    }
   }
   const bool weights = count && rank && ((da && k) || (db && n));
   if (da) r.vector(da, count * rank * k, 4, true);
@@ -373,7 +380,9 @@ int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank, int64
     if (rc != XPOSE_OK) return rc;
   }
   const int64_t used = some ? count : 0;
-  const bool beside = copies && weights && rank <= 32;
+  // Over dout or x, dx waits for the gradients, which read them.
+  const bool over = dx == dout || dx == x;
+  const bool beside = copies && weights && rank <= 32 && !over;
   const xpose::ExpandPlan plan = xpose::expand_plan(m, k, used, beside);
   xpose::ExpandArgs e{};
   e.h = dh;
@@ -395,10 +404,6 @@ int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank, int64
   e.slots = plan.slots;
   e.strips = (int32_t)plan.strips;
   e.alpha = 1.f;
-  if (copies && !beside) {
-    rc = hip(xpose::launch_expand(e, plan, dtype, dx_dtype, (hipStream_t)stream));
-    if (rc != XPOSE_OK || !weights) return rc;
-  }
   xpose::AdapterGradArgs g{};
   g.dh = dh;
   g.h = hidden;
@@ -419,8 +424,12 @@ int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank, int64
   g.count = (int32_t)count;
   g.piece = w.piece;
   g.alpha = alpha;
-  return hip(beside ? xpose::launch_adapter_both(e, plan, g, dtype, dx_dtype, (hipStream_t)stream)
-                    : xpose::launch_adapter_grad(g, dtype, (hipStream_t)stream));
+  if (beside) return hip(xpose::launch_adapter_both(e, plan, g, dtype, dx_dtype, (hipStream_t)stream));
+  if (weights) {
+    rc = hip(xpose::launch_adapter_grad(g, dtype, (hipStream_t)stream));
+    if (rc != XPOSE_OK) return rc;
+  }
+  return copies ? hip(xpose::launch_expand(e, plan, dtype, dx_dtype, (hipStream_t)stream)) : XPOSE_OK;
 }
 
 // ----- dropout ---------------------------------------------------------------------------
@@ -432,11 +441,11 @@ int xpose_dropout(int64_t rows, int64_t cols, const void *x, int64_t ldx, int32_
   const int size = size_of(dtype);
   if (!size) return XPOSE_EDTYPE;
   Ranges r;
-  r.matrix(x, rows, cols, ldx, size, size, false);
-  if (residual) r.matrix(residual, rows, cols, ld_residual, size, size, false);
-  r.matrix(y, rows, cols, ldy, size, size, true);
-  r.same(x, y);
-  r.same(residual, y);
+  const int in = r.matrix(x, rows, cols, ldx, size, size, false);
+  const int res = residual ? r.matrix(residual, rows, cols, ld_residual, size, size, false) : -1;
+  const int out = r.matrix(y, rows, cols, ldy, size, size, true);
+  r.same(in, out);
+  r.same(res, out);
   if (device_seed) r.vector(device_seed, 1, 8, false);
   const int rc = r.check();
   if (rc != XPOSE_OK || rows == 0 || cols == 0) return rc;

@@ -260,12 +260,12 @@ static int layer_norm(int64_t rows, int64_t cols, const void *x, int64_t ldx,
   const int size = size_of(dtype), param = size_of(param_dtype);
   if (!size || !param) return XPOSE_EDTYPE;
   Ranges r;
-  r.matrix(x, rows, cols, ldx, size, size, false);
+  const int in = r.matrix(x, rows, cols, ldx, size, size, false);
   if (weight) r.vector(weight, cols, param, false);
   if (bias) r.vector(bias, cols, param, false);
-  r.matrix(y, rows, cols, ldy, quantized ? 1 : size, quantized ? 8 : size, true);
+  const int out = r.matrix(y, rows, cols, ldy, quantized ? 1 : size, quantized ? 8 : size, true);
   if (quantized) r.matrix(scale, ceil_div(cols, kBlock), rows, ld_scale, 4, 4, true);
-  else r.same(x, y);
+  else r.same(in, out);
   if (mean && cols) {
     r.vector(mean, rows, 4, true);
     r.vector(rstd, rows, 4, true);
@@ -346,15 +346,16 @@ int xpose_layer_norm_backward(int64_t rows, int64_t cols, const void *dy,
   if (rc != XPOSE_OK) return rc;
   if (!xpose::norm_bwd_fits(rows, cols)) return XPOSE_EINVAL;
   Ranges r;
-  r.matrix(dy, rows, cols, lddy, size, size, false);
-  r.matrix(x, rows, cols, ldx, size, size, false);
+  const int in = r.matrix(dy, rows, cols, lddy, size, size, false);
+  const int in_x = r.matrix(x, rows, cols, ldx, size, size, false);
   if (cols) {
     r.vector(mean, rows, 4, false);
     r.vector(rstd, rows, 4, false);
   }
   if (weight) r.vector(weight, cols, param, false);
-  r.matrix(dx, rows, cols, lddx, size, size, true);
-  r.same(dy, dx);
+  const int out = r.matrix(dx, rows, cols, lddx, size, size, true);
+  r.same(in, out);
+  if (dy == dx) r.same(in_x, out);  // x may be dy: both are read before dx is written there
   if (dweight) r.vector(dweight, cols, 4, true);
   if (dbias) r.vector(dbias, cols, 4, true);
   const bool enough = workspace && workspace_bytes / 4 >= floats;

@@ -30,10 +30,11 @@ class Ranges {
  public:
   // rows x cols elements of `size` bytes with a pitch of ld elements.  The
   // pitch is checked for empty matrices too, as far as it has rows to bridge.
-  void matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int size,
-              int align, bool output) {
+  // The range's number, -1 where there is none.
+  int matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int size,
+             int align, bool output) {
     if (ld < (cols > 1 ? cols : 1)) rc_ = XPOSE_EINVAL;
-    if (rc_ != XPOSE_OK || rows == 0 || cols == 0) return;
+    if (rc_ != XPOSE_OK || rows == 0 || cols == 0) return -1;
     int64_t last, bytes;
     uintptr_t end;
     if (!p || __builtin_mul_overflow(rows - 1, ld, &last) ||
@@ -41,11 +42,12 @@ class Ranges {
         __builtin_mul_overflow(last, (int64_t)size, &bytes) ||
         __builtin_add_overflow((uintptr_t)p, (uintptr_t)bytes, &end)) {
       rc_ = XPOSE_EINVAL;
-      return;
+      return -1;
     }
     if ((uintptr_t)p % align) late(XPOSE_EALIGN);
     if (rows > 1 && ld * size % align) late(XPOSE_EALIGN);
-    all_[count_++] = {(uintptr_t)p, end, output, ld};
+    all_[count_] = {(uintptr_t)p, end, output, ld};
+    return count_++;
   }
   // An input of `count` such matrices, `stride` elements from one to the next.
   void matrices(const void *p, int64_t count, int64_t stride, int64_t rows,
@@ -60,12 +62,13 @@ class Ranges {
         __builtin_add_overflow(all_[before].hi, (uintptr_t)more, &all_[before].hi))
       rc_ = XPOSE_EINVAL;
   }
-  void vector(const void *p, int64_t n, int size, bool output) {
-    matrix(p, 1, n, n > 1 ? n : 1, size, size, output);
+  int vector(const void *p, int64_t n, int size, bool output) {
+    return matrix(p, 1, n, n > 1 ? n : 1, size, size, output);
   }
-  // `out` may also be `in` itself.
-  void same(const void *in, const void *out) {
-    if (in == out) in_place_[places_++] = (uintptr_t)in;
+  // The output `out` may also be the input `in` itself: these two, not what
+  // else lies there.
+  void same(int in, int out) {
+    if (in >= 0 && out >= 0) in_place_[places_++] = {in, out};
   }
   int check() const {
     if (rc_ != XPOSE_OK || late_ != XPOSE_OK) return rc_ != XPOSE_OK ? rc_ : late_;
@@ -73,9 +76,7 @@ class Ranges {
       for (int j = i + 1; j < count_; ++j) {
         const Range &a = all_[i], &b = all_[j];
         if (!(a.output || b.output) || a.lo >= b.hi || b.lo >= a.hi) continue;
-        if (in_place(a.lo) && a.lo == b.lo && a.hi == b.hi && a.ld == b.ld &&
-            a.output != b.output)
-          continue;
+        if (in_place(i, j) && a.lo == b.lo && a.hi == b.hi && a.ld == b.ld) continue;
         return XPOSE_EALIAS;
       }
     return XPOSE_OK;
@@ -87,14 +88,17 @@ class Ranges {
     bool output;
     int64_t ld;
   };
-  bool in_place(uintptr_t p) const {
-    for (int i = 0; i < places_; ++i)
-      if (in_place_[i] == p) return true;
+  struct Pair {
+    int in, out;
+  };
+  bool in_place(int i, int j) const {
+    for (int p = 0; p < places_; ++p)
+      if ((in_place_[p].in == i && in_place_[p].out == j) || (in_place_[p].in == j && in_place_[p].out == i)) return true;
     return false;
   }
   void late(int rc) { if (late_ == XPOSE_OK) late_ = rc; }
   Range all_[16];  // no call has more
-  uintptr_t in_place_[4];
+  Pair in_place_[4];
   int count_ = 0, places_ = 0;
   int rc_ = XPOSE_OK, late_ = XPOSE_OK;
 };
