@@ -600,20 +600,22 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(ShrinkArgs a) {
 constexpr int kExpandWaves = 4, kExpandThreads = 64 * kExpandWaves;
 constexpr int kExpandCols = 128;  // of a wave
 
-// Eight float32 numbers as operands of multiply_split.
+// Eight float32 numbers as operands of multiply_split.  The first part is cut
+// off, not rounded: the nearest bfloat16 of what lies over its largest number is
+// infinite.  The other two are rounded, which leaves nothing of 24 bits.
 template <typename T> struct Split8 {
   bf16x8 part[3];
   __device__ void set(const float (&f)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float rest = f[e];
+      const __bf16 first = __builtin_bit_cast(__bf16, (uint16_t)(__float_as_uint(f[e]) >> 16));
+      // an infinity is one, and not one less itself; of a NaN the rest is one too
+      float rest = __builtin_fabsf(f[e]) == __builtin_inff() ? 0.f : f[e] - (float)first;
+      part[0][e] = first;
 #pragma unroll
-      for (int p = 0; p < 3; ++p) {
-        const __bf16 b = (__bf16)rest;
-        part[p][e] = b;
-        rest -= (float)b;
-        // an infinity is one, and not one less itself
-        if (!(__builtin_fabsf((float)b) < __builtin_inff())) rest = 0.f;
+      for (int p = 1; p < 3; ++p) {
+        part[p][e] = (__bf16)rest;
+        rest -= (float)part[p][e];
       }
     }
   }
