@@ -86,8 +86,8 @@ int xpose_rms_norm_backward_workspace(int64_t rows, int64_t cols,
  * m x rank float32 values, dense.  ids: m values.
  *
  * hidden is summed in float32 and stays float32; out is formed in float32 and
- * rounded once.  Where hidden or B holds an infinity, what it goes into is
- * infinite or NaN.  Nothing of a row goes into another one.
+ * rounded once.  Where hidden, B or scale holds an infinity, what it goes into
+ * is infinite or NaN.  Nothing of a row goes into another one.
  *
  * m <= 2^26, n and k <= 2^30, rank <= 4096, count <= 65535. */
 int xpose_adapters(int64_t m, int64_t n, int64_t k, int64_t rank,

@@ -810,10 +810,14 @@ __device__ __forceinline__ void expand(const ExpandArgs &a, uint32_t block, uint
         }
         if (!mine) continue;
         Vec8<float> raw = c == 0 ? now.h : load_h(row0, c);
+        // ranks past the last one stay zeros whatever the factor is
+        const int ranks = SHORT ? valid8(a.rank - c - 8 * g) : 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) raw.v[e / 4][e % 4] = e < ranks ? raw.v[e / 4][e % 4] * factor : 0.f;
         if constexpr (!SHORT) settle8<float>(raw, a.rank, c + 8 * g);
         float f[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = at8<float>(raw, e) * factor;
+        for (int e = 0; e < 8; ++e) f[e] = at8<float>(raw, e);
         Split8<T> h;
         h.set(f);
 #pragma unroll

@@ -1,6 +1,8 @@
 """Values at the ends of their types in a residual block's operators: what is
 finite in float32 stays finite, numbers that are not there (ranks past the last
 one) reach nothing, zeros keep their sign."""
+import math
+
 import pytest
 
 from test_gpu_block import BF16, F16, F32, TYPES, _dev
@@ -86,3 +88,25 @@ def test_all_bits_of_hidden(dtype):
     _, _, db = X.adapters_backward(one, one, _full(0.0, 1, 16, 8, dtype=dtype).expand(4000, 16, 8),
                                    _full(0.0, 1, 8, 16, dtype=dtype).expand(4000, 8, 16), ids, hidden)
     assert torch.equal(db, hidden[:, None].expand(4000, 8, 16))
+
+
+@pytest.mark.parametrize("dtype,out", [(F32, F32), (F16, F16), (F16, F32), (BF16, BF16), (BF16, F32)])
+@pytest.mark.parametrize("rank", [1, 5, 8, 16, 31, 32, 40, 64])
+def test_an_infinite_scale(dtype, out, rank):
+    """Infinities of the products' sign, whatever the rank: numbers past the
+    last one are not multiplied by it, and other adapters' rows stay.  (float16
+    weights are the sum of two numbers, one of them 0 here: a NaN is right too.)"""
+    m, n, k = 12, 130, 64
+    gen = torch.Generator(device=_dev()).manual_seed(rank)
+    ids = torch.arange(m, dtype=torch.int32, device=_dev()) % 3 - 1
+    x, a = _full(1.0, m, k, dtype=dtype), _full(0.5, 2, rank, k, dtype=dtype)
+    b = torch.where(torch.rand(2, n, 1, generator=gen, device=_dev()) < 0.5, -1.0, 1.0).to(dtype).repeat(1, 1, rank)
+    base = torch.randn(m, n, generator=gen, device=_dev()).to(out)
+    say(f"infinite scale {dtype} {out} {rank}")
+    got = X.adapters(x, a, b, ids, base=base, scale=torch.tensor([1.0, math.inf], device=_dev()))
+    want = X.adapters(x, a, b, ids, base=base, scale=torch.tensor([1.0, 1.0], device=_dev()))
+    assert torch.equal(got[ids != 1], want[ids != 1])
+    if dtype == F16:
+        assert not got[ids == 1].isfinite().any()
+        return
+    assert torch.equal(got[ids == 1].float(), (b[1, :, 0].float() * math.inf).expand(int((ids == 1).sum()), n))
