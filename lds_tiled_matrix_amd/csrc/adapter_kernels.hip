@@ -1154,7 +1154,8 @@ __global__ __launch_bounds__(kDropThreads) void dropout_kernel(DropoutArgs a) {
                         (uint32_t)(seed >> 32));
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      y[e] = random.bits(e) >= a.threshold ? x[e] * a.factor : 0.f;
+      // -0 added to a residual leaves each as it is, a 0 loses a zero's sign
+      y[e] = random.bits(e) >= a.threshold ? x[e] * a.factor : RES ? -0.f : 0.f;
       if constexpr (RES) y[e] += r[e];
     }
     store8((T *)a.y + row * a.ldy + col, valid, y);

@@ -110,3 +110,15 @@ def test_an_infinite_scale(dtype, out, rank):
         assert not got[ids == 1].isfinite().any()
         return
     assert torch.equal(got[ids == 1].float(), (b[1, :, 0].float() * math.inf).expand(int((ids == 1).sum()), n))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_dropped_elements_are_the_residual(dtype):
+    """Bit for bit: a zero of it keeps its sign."""
+    x = torch.randn(50, 300, device=_dev()).to(dtype)
+    res = torch.where(torch.rand(50, 300, device=_dev()) < 0.5, -0.0, 0.0).to(dtype)
+    keep = X.dropout(torch.ones_like(x), 0.5, 3) != 0
+    y = X.dropout(x, 0.5, 3, residual=res)
+    assert not keep.all() and torch.equal(y.signbit()[~keep], res.signbit()[~keep]) and not y[~keep].any()
+    assert torch.equal(X.dropout(x, 1.0, 3, residual=res).signbit(), res.signbit())
+    assert not X.dropout(-x.abs(), 1.0, 3).signbit().any()  # zeros without one
