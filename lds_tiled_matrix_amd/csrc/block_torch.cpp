@@ -154,6 +154,17 @@ Matrices matrices(const Tensor &t, const char *what) {
   return {count, rows, cols, rows > 1 ? t.stride(1) : std::max<int64_t>(cols, 1), count > 1 ? t.stride(0) : 0};
 }
 
+// A number of the caller's that may be a tensor too; of another type it is a TypeError.
+template <typename T>
+T number(const py::object &given, const char *what) {
+  try {
+    return given.cast<T>();
+  } catch (const py::cast_error &) {
+    bad_type(std::string(what) + ": expected a number or a tensor, got " +
+             py::str(py::type::of(given).attr("__name__")).cast<std::string>());
+  }
+}
+
 // What a row's adapter is and is worth.
 struct Adapters {
   Matrices a, b;
@@ -184,7 +195,7 @@ Adapters adapters_of(const Tensor &first, const Tensor &a, const Tensor &b, cons
     same_device(first, *r.scales);
     r.scale = statistics(*r.scales, r.a.count, "scale");
   } else {
-    r.alpha = (float)scale.cast<double>();
+    r.alpha = (float)number<double>(scale, "scale");
   }
   return r;
 }
@@ -313,7 +324,7 @@ Tensor dropout(const Tensor &x, double p, const py::object &seed, uint64_t offse
       bad_type(std::string("seed: expected int64, got ") + c10::toString(device_seed->scalar_type()));
     if (device_seed->numel() != 1) bad_value("seed: expected one value");
   } else {
-    host_seed = seed.cast<uint64_t>();
+    host_seed = number<uint64_t>(seed, "seed");
   }
   const Stream on(x, stream);
   Tensor out = given ? *given : empty({mx.rows, mx.cols}, x.scalar_type(), x);

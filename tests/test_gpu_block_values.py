@@ -122,3 +122,17 @@ def test_dropped_elements_are_the_residual(dtype):
     assert not keep.all() and torch.equal(y.signbit()[~keep], res.signbit()[~keep]) and not y[~keep].any()
     assert torch.equal(X.dropout(x, 1.0, 3, residual=res).signbit(), res.signbit())
     assert not X.dropout(-x.abs(), 1.0, 3).signbit().any()  # zeros without one
+
+
+@pytest.mark.parametrize("call", [
+    lambda z, i: X.adapters(z(4, 8), z(2, 3, 8), z(2, 5, 3), i(4), scale="1"),
+    lambda z, i: X.adapters(z(4, 8), z(2, 3, 8), z(2, 5, 3), i(4), scale=None),
+    lambda z, i: X.adapters(z(4, 8), z(2, 3, 8), z(2, 5, 3), i(4), scale=[1.0, 2.0]),
+    lambda z, i: X.adapters_backward(z(4, 5), z(4, 8), z(2, 3, 8), z(2, 5, 3), i(4), z(4, 3), scale=(1.0,)),
+    lambda z, i: X.dropout(z(4, 4), 0.5, 1.5),
+    lambda z, i: X.dropout(z(4, 4), 0.5, None),
+    lambda z, i: X.dropout(z(4, 4), 0.5, "1"),
+])
+def test_numbers_of_another_type(call):
+    with pytest.raises(TypeError):
+        call(lambda *s: torch.zeros(*s, device=_dev()), lambda m: torch.zeros(m, dtype=torch.int32, device=_dev()))
