@@ -150,6 +150,23 @@ hipError_t launch(const void *kernel, const RmsNormArgs &a, dim3 grid, int threa
   void *args[] = {&copy};
   return hipLaunchKernel(kernel, grid, dim3(threads), args, 0, s);
 }
+// Whether half of the workgroups that fit on a compute unit, `half`, are enough
+// for rows of `bytes` that leave as a tensor: more rows at a time than keep memory
+// busy cost it.  A unit needs 24 KB of rows under way so, and 12 KB more for one
+// workgroup alone, which has a row at a time and waits for its sum; 10 KB and 20 KB
+// where each has 16 rows to go through, and the first and last ones count less.
+// To e4m3 the arithmetic needs them all (4096 x 8192 53 us and 43).
+//
+// All and half, in us: bfloat16 with the residual, one workgroup of two, 14826 x
+// 4519 127 and 162, 10468 x 6400 100 and 104, 9054 x 7400 102 and 104, 8723 x 7680
+// 100 and 99.5, 8186 x 8184 102 and 98, 1000 x 8192 11.3 and 12.3; float32 so 7413 x
+// 4519 107 and 105, 4154 x 8064 108 and 100, 700 x 6144 14.4 and 13.6.  Without it,
+// four of eight, bfloat16 55833 x 1200 55 and 69, 43619 x 1536 50 and 54, 32714 x
+// 2048 49 and 46, 5000 x 2048 8.2 and 9.6, 2000 x 4096 7.5 and 6.7.
+bool half_will_do(int64_t rows, int64_t bytes, int half) {
+  const int64_t under_way = bytes * half, kb = 1024;
+  return under_way >= 24 * kb + 12 * kb / half || (rows >= 16 * 256 * half && under_way >= 10 * kb + 20 * kb / half);
+}
 template <typename T, Out OUT, bool RES, int TR, int NC, bool SHORT = false>
 hipError_t launch_rms(const RmsNormArgs &a, hipStream_t s) {
   constexpr int per = norm_threads(TR) / TR;
@@ -163,13 +180,8 @@ hipError_t launch_rms(const RmsNormArgs &a, hipStream_t s) {
     else
       n = 1;
   }
-  // Long rows that leave as a tensor keep memory busy with half of that, and more
-  // rows at a time cost it: with the residual 8192 x 8192 bfloat16 takes 95 us and
-  // 99 with all, 3001 x 2999 float32 28 and 30, 4096 x 4096 bfloat16 23.5 and 25,
-  // without it 16384 x 2048 bfloat16 24 and 27.  Not where one workgroup would be
-  // left with idle lanes (12345 x 6789 bfloat16 158 and 151), and to e4m3 the
-  // arithmetic needs them all (4096 x 8192 53 and 43).
-  if (OUT == kTensor && TR > 64 && (n > 2 || a.cols == TR * NC * 8)) n = (n + 1) / 2;
+  if (OUT == kTensor && TR > 64 && half_will_do(a.rows, a.cols * (int64_t)sizeof(T) * (RES ? 2 : 1), (n + 1) / 2))
+    n = (n + 1) / 2;
   const int64_t grid = (a.rows + per - 1) / per, most = 256 * (int64_t)n;
   return launch(kernel, a, dim3((uint32_t)(grid < most ? grid : most)), norm_threads(TR), s);
 }
