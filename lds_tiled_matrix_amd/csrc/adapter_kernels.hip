@@ -45,15 +45,6 @@ constexpr int kBlock = 128;  // columns that share a scale of e4m3 x
 
 __device__ inline int valid8(int64_t left) { return left < 0 ? 0 : left > 8 ? 8 : (int)left; }
 
-// Eight elements from `col` on of a row of `len`: zeros beyond it.
-template <typename T>
-__device__ inline Vec8<T> guarded8(const T *row, int64_t len, int64_t col) {
-  if (len < 8) return load_raw8(row + col, valid8(len - col));
-  Vec8<T> v = load_row8(row, len, col);
-  settle8<T>(v, len, col);
-  return v;
-}
-
 // Chunks of 16 bytes: V of them from `col` on of a row of `len` elements.  As
 // with load_row8, what lies beyond the row's end is loaded from before it, and
 // settled into zeros later.
@@ -1086,14 +1077,14 @@ __global__ __launch_bounds__(kGradThreads) void adapter_grad_kernel(AdapterGradA
 // of both kinds share a compute unit (rank 64, pieces of 1024 rows, 158 us, 171 and
 // 242 here with 32 and 64 ranks a workgroup, float32 2048 rows 98 and 119).
 template <typename T, typename O, int NR, bool SHORT>
-__global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 && NR < 4 ? 2 : 1) void adapter_both_kernel(ExpandArgs e, AdapterGradArgs g, uint32_t expands) {
+__global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 ? 2 : 1) void adapter_both_kernel(ExpandArgs e, AdapterGradArgs g, uint32_t expands) {
   constexpr int kBytes = kExpandLds<T, 4> > NR * 8192 ? kExpandLds<T, 4> : NR * 8192;
   __shared__ __align__(16) uint8_t lds[kBytes];
   const uint32_t grads = gridDim.x - expands, pairs = min(expands, grads), block = blockIdx.x;
   const bool grad = block < 2 * pairs ? block % 2 : grads > expands;
   const uint32_t number = block < 2 * pairs ? block / 2 : block - pairs;
   if (grad) adapter_grad<T, NR, SHORT>(g, number, reinterpret_cast<f32x4 (*)[8][64]>(lds));
-  else if (blockIdx.y == 0) expand<T, O, 4, true, SHORT>(e, number, lds);
+  else expand<T, O, 4, true, SHORT>(e, number, lds);
 }
 
 // Adapters of several pieces get their sum.
@@ -1286,7 +1277,7 @@ hipError_t both(ExpandArgs e, const ExpandPlan &p, const AdapterGradArgs &a, con
   struct Tag;
   const void *kernel = reinterpret_cast<const void *>(&adapter_both_kernel<T, O, NR, SHORT>);
   const uint32_t expands = deal_out(e, p, groups_at_once<Tag>(kernel, kGradThreads));
-  return launch(kernel, dim3(expands + g.groups, g.chunks), kGradThreads, s, e, a, expands);
+  return launch(kernel, dim3(expands + g.groups), kGradThreads, s, e, a, expands);  // all ranks in one chunk
 }
 template <typename T, typename O, bool SHORT>
 hipError_t both(const ExpandArgs &e, const ExpandPlan &p, const AdapterGradArgs &a, const GradGrid &g, hipStream_t s) {
