@@ -1296,7 +1296,10 @@ ShrinkPlan shrink_plan(int64_t m, int64_t k, int64_t rank, int64_t count, int x_
   ShrinkPlan p{};
   // e4m3 rows take twice their bytes of weights: 32 of them a workgroup from where
   // those still fill the card (4096 columns, rank 16, 8192 rows 18.5 and 23 us,
-  // 16384 rows 32 and 40; but bfloat16 25 and 24, 5000 rows 25 and 21)
+  // 16384 rows 32 and 40; but bfloat16 25 and 24, 5000 rows 25 and 21).  Over 16
+  // ranks, of which 16 rows take 32 at a time and read x half as often, it makes little
+  // difference (both launches, 8192 rows, 4096 columns both ways, rank 32 54 us, 53
+  // with 16 rows, rank 64 77 both, rank 128 125 and 128).
   p.row_tiles = x_size == 1 && m > 4096 ? 2 : 1;
   const int64_t tiles = (m + 16 * p.row_tiles - 1) / (16 * p.row_tiles);
   // Few tiles: their adapters (16 of a tile at most) side by side, up to a
@@ -1320,9 +1323,14 @@ hipError_t launch_shrink(const ShrinkArgs &a, const ShrinkPlan &p, int dtype, hi
 ExpandPlan expand_plan(int64_t m, int64_t n, int64_t count, bool beside) {
   ExpandPlan p{};
   // Few rows leave waves down without any, but share h among fewer workgroups: 16
-  // tokens beside e4m3 10.6 us a call with 2, 11.1 with 1 and 11.3 with 4, 64 rows 9.3,
-  // 9.8 and 9.1 (4096 columns both ways).
-  p.waves_down = m > 16 || beside ? 4 : 2;
+  // tokens beside e4m3 10.6 us a call with 2, 11.1 with 1 and 11.3 with 4 (4096
+  // columns both ways).  More rows of few adapters share their operands among 4: 4000
+  // bfloat16 rows, 2048 to 4096 columns, rank 16, 16 adapters one after the other 28.3
+  // us, 29.7 with 2, in any order 138 and 145.  A tile of 64 rows goes through more of
+  // many adapters than one of 32 does: 32 of 64 rows 14.3 us, 11.9 with 2, of 4000 rows
+  // 31.5 and 30.9, in any order 215 and 198; 64 rows with one each 21.1 and 16.0, 256 of
+  // 512 rows 53.9 and 37.6.
+  p.waves_down = beside || (m > 16 && count < 32) ? 4 : 2;
   const int rows = 16 * p.waves_down, cols = kExpandCols * kExpandWaves / p.waves_down;
   p.strips = (n + cols - 1) / cols;
   p.tiles = (m + rows - 1) / rows;
@@ -1341,7 +1349,10 @@ hipError_t launch_expand(const ExpandArgs &a, const ExpandPlan &p, int dtype, in
 
 int adapter_grad_piece(int64_t m, int64_t n, int64_t k) {
   const int64_t tiles = (n + kGradCols - 1) / kGradCols + (k + kGradCols - 1) / kGradCols;
-  if (m <= 512) return 512;  // one piece an adapter: no second launch (300 rows 28 and 23 us a pass)
+  // One piece an adapter, no second launch: bfloat16, 4096 columns both ways, rank 12,
+  // 200 to 512 rows 15 to 17.6 us a pass, 19 to 23 with pieces of 128 rows, rank 64 38
+  // to 43 and 43 to 46; but one adapter of 400 float32 rows, 2999 and 1222, 27.3 and 24.4.
+  if (m <= 512) return 512;
   // a workgroup a compute unit, next to the other kernel's (8192 rows, 4096 columns
   // both ways, bfloat16: 128 rows a piece 130 us, 256 101, 512 92, 1024 85, 2048 82,
   // 4096 83; 2048 rows in float32: 128 55 us, 512 45, 2048 44)

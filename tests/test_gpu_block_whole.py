@@ -7,7 +7,7 @@ import pytest
 import oracle.block as ob
 import oracle.linear as ol
 from test_gpu_block import (BF16, F16, F32, TYPES, U32, _adapter_case, _backward_case, _block, _block_inputs,
-                            _check_adapters, _check_backward, _close, _dev, _norm_tol, _np, _terms, least, u)
+                            _check_adapters, _check_backward, _close, _dev, _norm_tol, _np, _run_backward, _terms, least, u)
 from xpose_testlib import say
 
 pytestmark = pytest.mark.gpu
@@ -153,3 +153,18 @@ def test_backward_of_few_rows_of_high_rank(m, rank, dtype):
     say(f"backward of few rows of high rank {m} {rank} {dtype}")
     ids = np.arange(m) % 7 - 1 if m > 1 else [3]
     _check_backward(_backward_case(m, 300, 600, rank, 6, dtype, dtype, m + rank, ids=ids), pads=(0,))
+
+
+@pytest.mark.parametrize("m,count", [(33, 31), (33, 32), (64, 32), (65, 40), (700, 33), (700, 300)])
+@pytest.mark.parametrize("rank", [16, 40])
+@pytest.mark.parametrize("dtype,out", [(F32, F32), (F16, F32), (BF16, BF16)])
+def test_many_adapters_of_several_tiles(m, count, rank, dtype, out):
+    """More rows than a tile, adapters one after the other and in any order,
+    forward and (dx alone too) backward."""
+    say(f"many adapters of several tiles {m} {count} {rank} {dtype}")
+    for ids in (np.arange(m) * count // m, np.random.default_rng(m).integers(-1, count, m)):
+        _check_adapters(_adapter_case(m, 270, 200, rank, count, dtype, out, m, ids=ids), pads=(0, 3))
+        c = _backward_case(m, 140, 270, rank, count, dtype, out, m, ids=ids)
+        _check_backward(c, pads=(0,))
+        whole, alone = _run_backward(c), _run_backward(c, wanted=(True, False, False))
+        assert torch.equal(alone[0], whole[0])
