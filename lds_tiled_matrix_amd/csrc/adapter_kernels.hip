@@ -1324,13 +1324,14 @@ ExpandPlan expand_plan(int64_t m, int64_t n, int64_t count, bool beside) {
   ExpandPlan p{};
   // Few rows leave waves down without any, but share h among fewer workgroups: 16
   // tokens beside e4m3 10.6 us a call with 2, 11.1 with 1 and 11.3 with 4 (4096
-  // columns both ways).  More rows of few adapters share their operands among 4: 4000
-  // bfloat16 rows, 2048 to 4096 columns, rank 16, 16 adapters one after the other 28.3
-  // us, 29.7 with 2, in any order 138 and 145.  A tile of 64 rows goes through more of
-  // many adapters than one of 32 does: 32 of 64 rows 14.3 us, 11.9 with 2, of 4000 rows
-  // 31.5 and 30.9, in any order 215 and 198; 64 rows with one each 21.1 and 16.0, 256 of
-  // 512 rows 53.9 and 37.6.
-  p.waves_down = beside || (m > 16 && count < 32) ? 4 : 2;
+  // columns both ways).  More rows share an adapter's operands among 4.  But of many
+  // adapters a tile of 64 rows goes through more than one of 32 does (bfloat16, 2048 to
+  // 4096 columns, rank 16: 32 adapters of 64 rows 14.3 us, 11.9 with 2, 64 rows with one
+  // each 21.1 and 16.0, 256 of 512 rows 53.9 and 37.6; 16 of 64 rows in any order 11.8
+  // and 12.2).  How many of them have rows is not known here: 512 rows of one take 10.5
+  // us, 10.8 with 2, and so may prompts, which have more rows and few adapters (4000
+  // rows of 8 in order 5% more with 2; 4000 of 32 in any order 8% less).
+  p.waves_down = beside || (m > 16 && (m > 512 || count < 32)) ? 4 : 2;
   const int rows = 16 * p.waves_down, cols = kExpandCols * kExpandWaves / p.waves_down;
   p.strips = (n + cols - 1) / cols;
   p.tiles = (m + rows - 1) / rows;
