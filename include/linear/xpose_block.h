@@ -54,9 +54,9 @@ int xpose_rms_norm_quantize(int64_t rows, int64_t cols, const void *x,
  * h is what the norm normalised.  dresidual (NULL: zeros) is the gradient that
  * h has from elsewhere; dx is then the gradient of x and of residual alike,
  * rounded once.  dy, h, dresidual and dx are of dtype; dweight is `cols`
- * float32 values, zeros when there are no rows.  dx may be dy or dresidual
- * itself (same pitch).  Over 8192 columns: ceil(cols / 2048) min(rows, 256) <
- * 2^24. */
+ * float32 values, zeros when there are no rows (the workspace is needed without
+ * it too).  dx may be dy or dresidual itself (same pitch).  Over 8192 columns:
+ * ceil(cols / 2048) min(rows, 256) < 2^24. */
 int xpose_rms_norm_backward(int64_t rows, int64_t cols, const void *dy,
                             int64_t lddy, const void *h, int64_t ldh,
                             int32_t dtype, const float *rstd,
@@ -115,9 +115,9 @@ int xpose_adapters_workspace(int64_t m, int64_t k, int64_t rank, int64_t count,
  * dx_dtype, dtype or XPOSE_F32; dx may be base itself (same pitch), and base
  * dout or x: the gradients are then formed before dx.  da and db: dense float32
  * of count x rank x k and count x n x rank, zeros for adapters of no row.  dx,
- * da and db may each be NULL: not wanted.  Sums are float32, in an order of
- * their own for each set of sizes and ids; where a term holds an infinity, its
- * sum is infinite or NaN.  Limits as above, and
+ * da and db may each be NULL: not wanted (the workspace is the same).  Sums are
+ * float32, in an order of their own for each set of sizes and ids; where a term
+ * holds an infinity, its sum is infinite or NaN.  Limits as above, and
  * (m / 4096 + count + 1) (ceil(n / 128) + ceil(k / 128)) < 2^23 - 256. */
 int xpose_adapters_backward(int64_t m, int64_t n, int64_t k, int64_t rank,
                             int64_t count, const void *dout, int64_t lddout,

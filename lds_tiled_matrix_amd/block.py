@@ -110,7 +110,8 @@ def adapters_backward(dout, x, a, b, ids, hidden, *, base=None, scale=1.0, wante
     shared product's gradient of x, and sets its dtype; ``out``, where dx goes,
     may be base itself (dout or x where that is base).  da and db are float32,
     shaped as a and b, zeros for adapters of no row.  ``wanted`` says which of
-    the three are: the others are None and cost nothing."""
+    the three are: the others are None and not computed; the workspace that the
+    call takes from torch's allocator is the same."""
     return tuple(_torch_side().adapters_backward(dout, x, a, b, ids, hidden, base, scale, list(wanted), out, stream))
 
 
