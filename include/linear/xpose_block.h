@@ -30,7 +30,9 @@ extern "C" {
  * weight (NULL: ones) is cols values of param_dtype.  rstd (NULL: not wanted)
  * is `rows` float32 values.  eps >= 0.  y and h may each be x or residual
  * themselves (same pitch), not the same one.  A row whose squares sum to over
- * float32 has rstd 0.  This and the next two: rows <= 2^31 - 1. */
+ * float32 has rstd 0; with eps 0, one whose squares are all under it has an
+ * infinite one, and y is infinite or NaN.  This and the next two: rows <=
+ * 2^31 - 1. */
 int xpose_rms_norm(int64_t rows, int64_t cols, const void *x, int64_t ldx,
                    int32_t dtype, const void *residual, int64_t ld_residual,
                    void *h, int64_t ldh, const void *weight,

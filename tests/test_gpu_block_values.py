@@ -136,3 +136,15 @@ def test_dropped_elements_are_the_residual(dtype):
 def test_numbers_of_another_type(call):
     with pytest.raises(TypeError):
         call(lambda *s: torch.zeros(*s, device=_dev()), lambda m: torch.zeros(m, dtype=torch.int32, device=_dev()))
+
+
+@pytest.mark.parametrize("cols", [5, 100, 3000, 20000])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_of_squares_outside_float32(cols, dtype):
+    """Over it rstd is 0; under it infinite with eps 0, and eps's with one."""
+    x = torch.stack([_full(v, cols, dtype=dtype) for v in (1e30, 1e-30, 0.0, 1.0)])
+    y, rstd = X.rms_norm(x, eps=0.0, stats=True)
+    assert rstd.tolist() == [0.0, float("inf"), float("inf"), 1.0]
+    assert not y[0].any() and y[1].isinf().all() and y[2].isnan().all() and (y[3] == 1).all()
+    y, rstd = X.rms_norm(x, eps=0.25, stats=True)
+    assert rstd[:3].tolist() == [0.0, 2.0, 2.0] and not y[0].any() and torch.equal(y[1], x[1] * 2) and not y[2].any()
